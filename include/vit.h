@@ -18,7 +18,10 @@
  * Around the stack: patch embedding and bilinear position-table
  * interpolation (the steps before it), a CUDA-graph capture of any sequence
  * of calls, and an MXFP8 block-scaled linear layer (E4M3 codes, one E8M0
- * scale per 32 elements) with its quantiser.
+ * scale per 32 elements) with its quantiser.  For layers of newer towers:
+ * RMSNorm with the residual's addition (its output in the context's type or
+ * in MXFP8), an MXFP4 linear layer (E2M1 codes) with its quantiser, and RoPE
+ * over three axes (time, row, column).
  *
  * Conventions (all entry points):
  *  - Every tensor pointer is a DEVICE pointer owned by the caller, unless the
@@ -28,7 +31,8 @@
  *  - Activations are row-major [tokens, features] with contiguous rows.
  *    Weights use the [out_features, in_features] row-major layout.
  *  - Element type of every floating tensor = vit_config.dtype (fp32 or bf16);
- *    the MXFP8 entry points take byte codes and scales as documented there.
+ *    the MXFP8 and MXFP4 entry points take byte codes and scales as
+ *    documented there.
  *    bf16 runs tcgen05 tensor-core kernels with fp32 accumulation; fp32 runs
  *    SIMT FFMA kernels (no TF32).
  *  - Streams are passed as void* (a cudaStream_t; NULL = legacy stream).  All
@@ -342,6 +346,21 @@ VIT_API vit_status vit_layernorm(vit_ctx *ctx, const void *x, void *y,
                          const void *gamma, const void *beta, int rows,
                          int cols, float eps, void *stream);
 
+/* RMSNorm with the residual's addition, for layers that normalise by the root
+ * mean square in place of LayerNorm:
+ *   h = x + residual   (rounded once to the element type, as stored)
+ *   y = h / sqrt(mean(h^2) + eps) * gamma
+ * x, residual, h, y [rows, cols]; gamma [cols].  residual may be NULL (h = x);
+ * h may be NULL when the sum is not needed again.  The squares are summed in
+ * fp64; a bf16 y is the correctly rounded value of the formula for the stored
+ * h.  h and y may each be the same buffer as x or residual (in place), but not
+ * each other; any other overlap is VIT_ERR_INVALID_ARG.  All pointers 16-byte
+ * aligned (fp32 too), eps >= 0.  cols a multiple of 8 (bf16) or 4 (fp32), at
+ * most 16384, else VIT_ERR_UNSUPPORTED. */
+VIT_API vit_status vit_rmsnorm(vit_ctx *ctx, const void *x, const void *residual,
+                               const void *gamma, void *h, void *y, int rows, int cols, float eps,
+                               void *stream);
+
 /* Epilogues of vit_linear */
 typedef enum {
   VIT_EPI_BIAS = 0,           /* y = x W^T + b                               */
@@ -362,6 +381,35 @@ VIT_API vit_status vit_linear(vit_ctx *ctx, const void *x, const void *w,
  * theta^(-2j/h). */
 VIT_API vit_status vit_rope2d(vit_ctx *ctx, void *qkv, const int32_t *pos_rc,
                       int total_tokens, void *stream);
+
+/* RoPE over three axes, for images and video: pos_thw [T, 3] = (time, row,
+ * column) of each token.  A head's d/2 rotated pairs (d = cfg.head_dim) each
+ * have an axis and a frequency f; pair (a, b) at position p of its axis becomes
+ *   (a cos(p f) - b sin(p f), b cos(p f) + a sin(p f)).
+ * sections_host: HOST int32[3], the pairs of each axis (>= 0, their sum d/2).
+ * Layouts, theta = cfg.rope_theta:
+ *   VIT_ROPE_BLOCKS    axis a rotates its own 2 sections[a] consecutive dims;
+ *                      in that block dim j pairs with j + sections[a], f =
+ *                      theta^(-j / sections[a]).  (0, d/4, d/4) is vit_rope2d.
+ *   VIT_ROPE_SECTIONS  dim j < d/2 pairs with j + d/2, f = theta^(-2j/d); the
+ *                      first sections[0] pairs are time's, the next row's,
+ *                      then column's.
+ *   VIT_ROPE_TURNS     the same pairs and frequencies; the axes take them in
+ *                      turn (time, row, column, time, ...), an axis that has
+ *                      its share being passed over.
+ * x [T, heads, d] with x_stride elements from a token to the next (the rotated
+ * heads may be the front of a wider row: [T, 3, H, d] takes heads = 2H, x_stride
+ * = 3 H d); y likewise with y_stride.  y = x with equal strides rotates in
+ * place; otherwise no element of x may be written (slices of one wider row that
+ * do not meet are fine).  Other elements of y's rows are left as they are.
+ * Angles are reduced in 64-bit fixed point: within 1e-6 of the formula's at any
+ * int32 position (1e-7 below 2^21).  Strides >= heads * d, pointers
+ * aligned to the element (16-byte aligned rows are fastest). */
+typedef enum { VIT_ROPE_BLOCKS = 0, VIT_ROPE_SECTIONS = 1, VIT_ROPE_TURNS = 2 } vit_rope_layout;
+VIT_API vit_status vit_rope3d(vit_ctx *ctx, const void *x, long long x_stride, void *y,
+                              long long y_stride, const int32_t *pos_thw, int total_tokens,
+                              int heads, const int32_t *sections_host, vit_rope_layout layout,
+                              void *stream);
 
 /* ---- MXFP8 (block-scaled 8-bit) linear layer ----
  * The pages name 8-bit inference as a next step without fixing a format (the
@@ -400,12 +448,60 @@ VIT_API vit_status vit_layernorm_mx8(vit_ctx *ctx, const void *x, const void *ga
                                      const void *beta, int rows, int cols, float eps, void *codes,
                                      void *scales, void *stream);
 
+/* RMSNorm straight to MXFP8: h as vit_rmsnorm writes it, and codes, scales =
+ * vit_mx8_quantize(y of vit_rmsnorm), bit for bit, in one launch.  bf16
+ * contexts; cols a multiple of 8, at most 16384 (else VIT_ERR_UNSUPPORTED);
+ * codes and scales overlap nothing else; otherwise as vit_rmsnorm. */
+VIT_API vit_status vit_rmsnorm_mx8(vit_ctx *ctx, const void *x, const void *residual,
+                                   const void *gamma, void *h, int rows, int cols, float eps,
+                                   void *codes, void *scales, void *stream);
+
 /* y bf16 [M, N] = epi(deq(A) deq(W)^T + bias) with A = (a_codes, a_scales)
  * [M, K] and W = (w_codes, w_scales) [N, K] (a PyTorch Linear weight,
  * quantised along K); bias bf16 [N] or NULL; residual bf16 [M, N] for
  * VIT_EPI_BIAS_RESIDUAL.  fp32 accumulation on the tensor core (block-scaled
  * MMA).  N a multiple of 8.  Errors as vit_linear. */
 VIT_API vit_status vit_linear_mx8(vit_ctx *ctx, const void *a_codes, const void *a_scales,
+                                  const void *w_codes, const void *w_scales, const void *bias,
+                                  const void *residual, void *y, int M, int N, int K,
+                                  vit_epilogue epi, void *stream);
+
+/* ---- MXFP4 (block-scaled 4-bit) linear layer ----
+ * OCP Microscaling v1.0 MXFP4: E2M1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives), one E8M0 scale 2^(s-127) per 32 consecutive elements of a
+ * row; a quarter of bf16's bytes.  bf16 contexts only.
+ *
+ * codes  : [rows, vit_mx4_row_bytes(K)] bytes, two elements a byte: element
+ *          (r, k) in the low (even k) or high (odd k) nibble of byte
+ *          r * row_bytes + k / 2.  vit_mx4_row_bytes(K) = 16 ceil(K / 32);
+ *          the nibbles past K hold zero.
+ * scales : vit_mx4_scale_bytes(rows, K) bytes, the layout of the MXFP8
+ *          scales (512-byte blocks of 128 rows x 128 columns).  Byte 255 (NaN)
+ *          marks a group that holds a NaN.
+ * All buffers belong to the caller; device pointers 16-byte aligned. */
+VIT_API size_t vit_mx4_row_bytes(int K);
+VIT_API size_t vit_mx4_scale_bytes(int rows, int K);
+
+/* x bf16 [rows, K] (row stride K, any K) -> codes, scales; every byte of both
+ * is written.  Per 32-element group: X = floor(log2 max|x|) - 2 clamped to
+ * [-127, 127] (-127 for an all-zero group), code = E2M1(x / 2^X) rounded to
+ * nearest even, magnitudes above 6 (infinities too) clamped to 6; a group with
+ * a NaN has scale byte 255 and zero codes.  Errors as vit_mx8_quantize. */
+VIT_API vit_status vit_mx4_quantize(vit_ctx *ctx, const void *x, int rows, int K, void *codes,
+                                    void *scales, void *stream);
+
+/* codes, scales -> the values they stand for, bf16 y [rows, K] (exact: an E2M1
+ * value times a power of two; NaN for scale byte 255).  Errors as
+ * vit_mx4_quantize. */
+VIT_API vit_status vit_mx4_dequantize(vit_ctx *ctx, const void *codes, const void *scales,
+                                      int rows, int K, void *y, void *stream);
+
+/* y bf16 [M, N] = epi(deq(A) deq(W)^T + bias) with A = (a_codes, a_scales)
+ * [M, K] and W = (w_codes, w_scales) [N, K], both MXFP4 along K (any K >= 1);
+ * bias bf16 [N] or NULL; residual bf16 [M, N] for VIT_EPI_BIAS_RESIDUAL (may
+ * be y: in place).  fp32 accumulation on the tensor core (block-scaled MMA).
+ * N a multiple of 8.  Errors as vit_linear_mx8. */
+VIT_API vit_status vit_linear_mx4(vit_ctx *ctx, const void *a_codes, const void *a_scales,
                                   const void *w_codes, const void *w_scales, const void *bias,
                                   const void *residual, void *y, int M, int N, int K,
                                   vit_epilogue epi, void *stream);
@@ -451,7 +547,9 @@ typedef enum {
   VIT_K_MX8_QUANTIZE = 11, VIT_K_GEMM_MX8 = 12, /* vit_mx8_quantize, vit_linear_mx8 */
   VIT_K_ROWSTATS = 13, /* row statistics of a stack's input (folded LayerNorm) */
   VIT_K_FOLD = 14,     /* vit_fold_layernorm */
-  VIT_K_COUNT = 15
+  VIT_K_RMSNORM = 15,  /* vit_rmsnorm, vit_rmsnorm_mx8 (vit_rope3d: VIT_K_ROPE) */
+  VIT_K_MX4_QUANTIZE = 16, VIT_K_GEMM_MX4 = 17, /* vit_mx4_(de)quantize, vit_linear_mx4 */
+  VIT_K_COUNT = 18
 } vit_kernel_kind;
 
 /* enable != 0: every later kernel launch of this context is bracketed by two

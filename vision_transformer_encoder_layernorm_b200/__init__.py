@@ -19,7 +19,7 @@ __all__ = [
     "lib", "LIB_PATH", "VitError", "VitConfig", "VitLayerWeights", "VitProjectorWeights",
     "VitSeqs", "Context",
     "F32", "BF16", "FLAG_NO_ROPE", "FLAG_NO_MLP", "EPI_BIAS", "EPI_BIAS_GELU",
-    "EPI_BIAS_RESIDUAL", "STATUS", "ABI_FUNCTIONS", "KERNEL_KINDS", "Graph",
+    "EPI_BIAS_RESIDUAL", "ROPE_BLOCKS", "ROPE_SECTIONS", "ROPE_TURNS", "STATUS", "ABI_FUNCTIONS", "KERNEL_KINDS", "Graph",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libvit.so")
@@ -27,9 +27,10 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libvit.so")
 F32, BF16 = 0, 1
 FLAG_NO_ROPE, FLAG_NO_MLP = 0x1, 0x2
 EPI_BIAS, EPI_BIAS_GELU, EPI_BIAS_RESIDUAL = 0, 1, 2
+ROPE_BLOCKS, ROPE_SECTIONS, ROPE_TURNS = 0, 1, 2
 KERNEL_KINDS = ("layernorm", "gemm_qkv", "rope", "attention", "gemm_out", "gemm_fc1",
                 "gemm_fc2", "merge", "positions", "gemm", "embed", "mx8_quantize", "gemm_mx8",
-                "rowstats", "fold")
+                "rowstats", "fold", "rmsnorm", "mx4_quantize", "gemm_mx4")
 STATUS = {0: "VIT_OK", 1: "VIT_ERR_INVALID_ARG", 2: "VIT_ERR_SHAPE", 3: "VIT_ERR_UNSUPPORTED",
           4: "VIT_ERR_WORKSPACE", 5: "VIT_ERR_CUDA", 6: "VIT_ERR_TIMEOUT",
           7: "VIT_ERR_DEVICE_BOUNDS"}
@@ -122,6 +123,15 @@ ABI_FUNCTIONS = {
     "vit_mx8_quantize": (_I, [_P, _P, _I, _I, _P, _P, _P]),
     "vit_layernorm_mx8": (_I, [_P, _P, _P, _P, _I, _I, ctypes.c_float, _P, _P, _P]),
     "vit_linear_mx8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P]),
+    "vit_rmsnorm": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, ctypes.c_float, _P]),
+    "vit_rmsnorm_mx8": (_I, [_P, _P, _P, _P, _P, _I, _I, ctypes.c_float, _P, _P, _P]),
+    "vit_mx4_row_bytes": (ctypes.c_size_t, [_I]),
+    "vit_mx4_scale_bytes": (ctypes.c_size_t, [_I, _I]),
+    "vit_mx4_quantize": (_I, [_P, _P, _I, _I, _P, _P, _P]),
+    "vit_mx4_dequantize": (_I, [_P, _P, _P, _I, _I, _P, _P]),
+    "vit_linear_mx4": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P]),
+    "vit_rope3d": (_I, [_P, _P, ctypes.c_longlong, _P, ctypes.c_longlong, _P, _I, _I,
+                        ctypes.POINTER(ctypes.c_int32), _I, _P]),
     "vit_get_last_device_status": (_I, [_P]),
     "vit_debug_lost_tx": (_I, [_P, ctypes.c_uint]),
     "vit_status_string": (ctypes.c_char_p, [_I]),
@@ -175,6 +185,16 @@ def mx8_row_bytes(K: int) -> int:
 def mx8_scale_bytes(rows: int, K: int) -> int:
     """Bytes of the E8M0 scale blocks of a [rows, K] MXFP8 matrix."""
     return int(lib.vit_mx8_scale_bytes(rows, K))
+
+
+def mx4_row_bytes(K: int) -> int:
+    """Bytes per row of an MXFP4 code matrix with K columns."""
+    return int(lib.vit_mx4_row_bytes(K))
+
+
+def mx4_scale_bytes(rows: int, K: int) -> int:
+    """Bytes of the E8M0 scale blocks of a [rows, K] MXFP4 matrix."""
+    return int(lib.vit_mx4_scale_bytes(rows, K))
 
 
 def _grids_arr(grids: Sequence[Sequence[int]]):
@@ -236,6 +256,35 @@ class Context:
         h = ctypes.c_void_p()
         _check("vit_init", lib.vit_init(ctypes.byref(self.cfg), device, ctypes.byref(h)))
         self._h = h
+        self._device = device
+
+    # Checks of the entry points that take tensors of a fixed layout: the C call
+    # sees bare pointers, so a wrong type, device, shape or stride is refused here.
+    def _dense(self, fn: str, t, dtype, shape):
+        """t: a contiguous tensor of this type and shape on the context's device."""
+        if t.dtype != dtype or t.get_device() != self._device or not t.is_contiguous():
+            raise VitError(fn, 1)
+        if tuple(t.shape) != shape:
+            raise VitError(fn, 2)
+
+    def _bytes(self, fn: str, t, size: int):
+        """t: a contiguous byte tensor of at least `size` bytes on the device."""
+        import torch
+        if t.dtype != torch.uint8 or t.get_device() != self._device or not t.is_contiguous():
+            raise VitError(fn, 1)
+        if t.numel() < size:
+            raise VitError(fn, 2)
+
+    def _element(self):
+        import torch
+        return torch.bfloat16 if self.cfg.dtype == BF16 else torch.float32
+
+    def _on(self, stream):
+        """The given stream, or the current one of the context's device."""
+        if stream is None:
+            import torch
+            return torch.cuda.current_stream(self._device).cuda_stream
+        return stream if isinstance(stream, int) else stream.cuda_stream
 
     @property
     def handle(self):
@@ -378,6 +427,96 @@ class Context:
         _check("vit_linear_mx8", lib.vit_linear_mx8(self._h, _ptr(a[0]), _ptr(a[1]), _ptr(w[0]),
                                                     _ptr(w[1]), _ptr(bias), _ptr(residual), _ptr(y),
                                                     M, N, K, epi, _stream(stream)))
+
+    def _norm_args(self, fn, x, gamma, residual, h):
+        rows, cols = x.shape
+        dt = self._element()
+        self._dense(fn, x, dt, (rows, cols))
+        self._dense(fn, gamma, dt, (cols,))
+        for t in (residual, h):
+            if t is not None:
+                self._dense(fn, t, dt, (rows, cols))
+        return rows, cols
+
+    def rmsnorm(self, x, gamma, y, residual=None, h=None, eps=None, stream=None):
+        """vit_rmsnorm: y = h / sqrt(mean(h^2) + eps) * gamma of h = x +
+        residual (h = x without one); h, if given, receives the sum."""
+        rows, cols = self._norm_args("vit_rmsnorm", x, gamma, residual, h)
+        self._dense("vit_rmsnorm", y, x.dtype, (rows, cols))
+        e = self.cfg.ln_eps if eps is None else eps
+        _check("vit_rmsnorm", lib.vit_rmsnorm(self._h, _ptr(x), _ptr(residual), _ptr(gamma),
+                                              _ptr(h), _ptr(y), rows, cols, e, self._on(stream)))
+
+    def rmsnorm_mx8(self, x, gamma, codes, scales, residual=None, h=None, eps=None, stream=None):
+        """vit_rmsnorm_mx8: rmsnorm straight to MXFP8 codes / scales (the layout
+        of mx8_quantize)."""
+        rows, cols = self._norm_args("vit_rmsnorm_mx8", x, gamma, residual, h)
+        self._bytes("vit_rmsnorm_mx8", codes, rows * ((cols + 15) // 16 * 16))
+        self._bytes("vit_rmsnorm_mx8", scales, mx8_scale_bytes(rows, cols))
+        e = self.cfg.ln_eps if eps is None else eps
+        _check("vit_rmsnorm_mx8", lib.vit_rmsnorm_mx8(
+            self._h, _ptr(x), _ptr(residual), _ptr(gamma), _ptr(h), rows, cols, e, _ptr(codes),
+            _ptr(scales), self._on(stream)))
+
+    def _mx4_args(self, fn, pair, rows, K):
+        codes, scales = pair
+        self._bytes(fn, codes, rows * mx4_row_bytes(K))
+        self._bytes(fn, scales, mx4_scale_bytes(rows, K))
+
+    def mx4_quantize(self, x, codes, scales, stream=None):
+        """bf16 x [rows, K] -> MXFP4 codes [rows, mx4_row_bytes(K)] (uint8) and
+        scales [mx4_scale_bytes(rows, K)] (uint8), see vit_mx4_quantize."""
+        rows, K = x.shape
+        self._dense("vit_mx4_quantize", x, self._element(), (rows, K))
+        self._mx4_args("vit_mx4_quantize", (codes, scales), rows, K)
+        _check("vit_mx4_quantize", lib.vit_mx4_quantize(self._h, _ptr(x), rows, K, _ptr(codes),
+                                                        _ptr(scales), self._on(stream)))
+
+    def mx4_dequantize(self, codes, scales, y, stream=None):
+        """MXFP4 codes and scales of a [rows, K] matrix -> bf16 y [rows, K]."""
+        rows, K = y.shape
+        self._dense("vit_mx4_dequantize", y, self._element(), (rows, K))
+        self._mx4_args("vit_mx4_dequantize", (codes, scales), rows, K)
+        _check("vit_mx4_dequantize", lib.vit_mx4_dequantize(
+            self._h, _ptr(codes), _ptr(scales), rows, K, _ptr(y), self._on(stream)))
+
+    def linear_mx4(self, a, w, bias, y, K, epi=EPI_BIAS, residual=None, stream=None):
+        """y = epi(deq(A) deq(W)^T + bias) with a = (codes, scales) [M, K] and
+        w = (codes, scales) [N, K] from mx4_quantize."""
+        fn = "vit_linear_mx4"
+        M, N = y.shape
+        dt = self._element()
+        self._dense(fn, y, dt, (M, N))
+        self._mx4_args(fn, a, M, K)
+        self._mx4_args(fn, w, N, K)
+        if bias is not None:
+            self._dense(fn, bias, dt, (N,))
+        if residual is not None:
+            self._dense(fn, residual, dt, (M, N))
+        _check(fn, lib.vit_linear_mx4(self._h, _ptr(a[0]), _ptr(a[1]), _ptr(w[0]), _ptr(w[1]),
+                                      _ptr(bias), _ptr(residual), _ptr(y), M, N, K, epi,
+                                      self._on(stream)))
+
+    def rope3d(self, x, pos_thw, sections, layout=ROPE_BLOCKS, out=None, stream=None):
+        """vit_rope3d on x [T, heads, head_dim] (rows of a wider tensor may be
+        sliced: only the token stride is free), into ``out`` or in place."""
+        import torch
+        fn = "vit_rope3d"
+        T, heads, d = x.shape
+        y = x if out is None else out
+        for t in (x, y):
+            if t.dtype != self._element() or t.get_device() != self._device:
+                raise VitError(fn, 1)
+            if tuple(t.shape) != (T, heads, d) or d != self.cfg.head_dim or len(sections) != 3:
+                raise VitError(fn, 2)
+            if t.numel() and ((heads > 1 and t.stride(1) != d) or t.stride(2) != 1):
+                raise VitError(fn, 1)
+        self._dense(fn, pos_thw, torch.int32, (T, 3))
+        # a single token has no stride to go by
+        xs, ys = (max(t.stride(0), heads * d) if T <= 1 else t.stride(0) for t in (x, y))
+        sec = (ctypes.c_int32 * 3)(*sections)
+        _check(fn, lib.vit_rope3d(self._h, _ptr(x), xs, _ptr(y), ys, _ptr(pos_thw), T, heads, sec,
+                                  layout, self._on(stream)))
 
     def rope2d(self, qkv, pos_rc, stream=None):
         _check("vit_rope2d", lib.vit_rope2d(self._h, _ptr(qkv), _ptr(pos_rc), qkv.shape[0],

@@ -26,6 +26,7 @@
 
 #include <cuda_fp8.h>
 
+#include "gemm_common.cuh"
 #include "kernels.h"
 #include "mx8.h"
 #include "sm100.cuh"
@@ -88,25 +89,6 @@ struct __align__(16) Bars {
   int abort_flag;
 };
 static_assert(sizeof(Bars) <= kLnSlotsOffset, "barrier block overlaps the LayerNorm slots");
-
-__device__ __forceinline__ float tanh_fast(float x) {
-  float y;
-  asm("tanh.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ float gelu_fast(float u) {
-  const float k0 = 0.7978845608028654f, k1 = 0.044715f;
-  return 0.5f * u * (1.0f + tanh_fast(k0 * fmaf(k1 * u, u * u, u)));
-}
-
-// Waits bounded by time only (used while draining after an abort).
-__device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity) {
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(bar, parity)) {
-    if (globaltimer_ns() - t0 > 200000000ull) break;  // 200 ms
-  }
-}
 
 }  // namespace gemm
 
@@ -944,6 +926,21 @@ CUresult encode_tensor_map_2d(CUtensorMap *map, CUtensorMapDataType dt, const vo
   return encode(map, dt, 2, const_cast<void *>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+CUresult encode_tensor_map_3d(CUtensorMap *map, CUtensorMapDataType dt, const void *base,
+                              uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1_bytes,
+                              uint64_t stride2_bytes, uint32_t box0, uint32_t box1, uint32_t box2,
+                              CUtensorMapSwizzle swz) {
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  if (encode == nullptr) return CUDA_ERROR_NOT_FOUND;
+  cuuint64_t dims[3] = {d0, d1, d2};
+  cuuint64_t strides[2] = {stride1_bytes, stride2_bytes};
+  cuuint32_t box[3] = {box0, box1, box2};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return encode(map, dt, 3, const_cast<void *>(base), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 template <int BN, int EPI>

@@ -59,6 +59,31 @@ cudaError_t launch_positions(const ImageTable &tab, int n_images, int cu_offset_
 cudaError_t launch_rope2d(int dtype, void *qkv, const int32_t *pos, int T, int H, int d,
                           const RopeFreqs &fr, cudaStream_t st);
 
+// RMSNorm with an optional residual addition (k_rmsnorm.cu): h = x + res (h
+// may be null without res), y = h gamma / sqrt(mean(h^2) + eps); cols a
+// multiple of 8 (bf16) or 4 (fp32), at most 16384.  The MXFP8 form writes y as
+// codes and scales (layout as launch_mx8_quantize).
+cudaError_t launch_rmsnorm(int dtype, const void *x, const void *res, const void *gamma, void *h,
+                           void *y, int rows, int cols, float eps, cudaStream_t st);
+cudaError_t launch_rmsnorm_mx8(const void *x, const void *res, const void *gamma, void *h, int rows,
+                               int cols, float eps, uint8_t *codes, uint8_t *scales,
+                               cudaStream_t st);
+
+// Three-axis RoPE (k_rope3d.cu).  Pair p < d/2 of a head: dims lo and hi, the
+// axis whose position turns it, and its frequency / 2 pi in units of 2^-64
+// turns.
+constexpr int kRope3dMaxPairs = 64;
+struct Rope3dTable {
+  uint64_t turn[kRope3dMaxPairs];
+  uint8_t lo[kRope3dMaxPairs], hi[kRope3dMaxPairs], axis[kRope3dMaxPairs];
+};
+// x, y [tokens, heads, d] with token strides xs, ys in elements (y may be x);
+// pos [tokens, 3].  vec: elements of a run of pairs whose lo and hi dims are
+// consecutive from a multiple of vec (a power of two that divides d/2).
+cudaError_t launch_rope3d(int dtype, const void *x, long long xs, void *y, long long ys,
+                          const int32_t *pos, int tokens, int heads, int d, const Rope3dTable &tab,
+                          int vec, cudaStream_t st);
+
 // patch embedding inputs (k_embed.cu)
 cudaError_t launch_embed_inputs(int dtype, const ImageTable &tab, int n_images,
                                 long long max_tokens, const void *px, void *patches, int p, int kp,
@@ -210,5 +235,10 @@ inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, siz
 CUresult encode_tensor_map_2d(CUtensorMap *map, CUtensorMapDataType dt, const void *base,
                               uint64_t inner, uint64_t rows, uint64_t row_stride_bytes,
                               uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swz);
+// The same for a 3-D tensor (strides of the two outer dimensions in bytes).
+CUresult encode_tensor_map_3d(CUtensorMap *map, CUtensorMapDataType dt, const void *base,
+                              uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1_bytes,
+                              uint64_t stride2_bytes, uint32_t box0, uint32_t box1, uint32_t box2,
+                              CUtensorMapSwizzle swz);
 
 }  // namespace vit

@@ -22,6 +22,7 @@
 
 #include "../../include/vit.h"
 #include "kernels.h"
+#include "mx4.h"
 #include "mx8.h"
 
 // Launch accounting: a count per kernel kind, and (while enabled) a pair of
@@ -1050,6 +1051,245 @@ vit_status vit_encoder_forward_mx8(vit_ctx *ctx, const vit_layer_weights_mx8 *la
       return s;
   }
   return VIT_OK;
+}
+
+// ---------------------------------------------------------------- RMSNorm
+namespace {
+
+// Whether [a, a + na) and [b, b + nb) share a byte.
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return a && b && na && nb && p < q + nb && q < p + na;
+}
+
+// Arguments shared by both forms; y is null for the MXFP8 one.
+vit_status check_rmsnorm(const vit_ctx *ctx, const void *x, const void *residual,
+                         const void *gamma, const void *h, const void *y, int rows, int cols,
+                         float eps) {
+  if (rows < 0 || cols < 0 || !(eps >= 0.f)) return VIT_ERR_INVALID_ARG;
+  const bool bf16 = ctx->cfg.dtype == VIT_BF16;
+  if (cols % (bf16 ? 8 : 4) || cols > 16384) return VIT_ERR_UNSUPPORTED;
+  const void *ps[5] = {x, residual, gamma, h, y};
+  for (const void *p : ps)
+    if (p && !aligned16(p)) return VIT_ERR_INVALID_ARG;
+  // outputs may take an input's place row by row, and nothing else
+  const size_t n = size_t(rows) * cols * esize(ctx->cfg), ng = size_t(cols) * esize(ctx->cfg);
+  const void *outs[2] = {h, y};
+  for (const void *o : outs) {
+    if ((o != x && overlap(o, n, x, n)) || (o != residual && overlap(o, n, residual, n)) ||
+        overlap(o, n, gamma, ng))
+      return VIT_ERR_INVALID_ARG;
+  }
+  return overlap(h, n, y, n) ? VIT_ERR_INVALID_ARG : VIT_OK;
+}
+
+}  // namespace
+
+vit_status vit_rmsnorm(vit_ctx *ctx, const void *x, const void *residual, const void *gamma,
+                       void *h, void *y, int rows, int cols, float eps, void *stream) {
+  if (!ctx || !x || !gamma || !y) return VIT_ERR_INVALID_ARG;
+  const vit_status s = check_rmsnorm(ctx, x, residual, gamma, h, y, rows, cols, eps);
+  if (s != VIT_OK) return s;
+  if (rows == 0 || cols == 0) return VIT_OK;
+  DeviceGuard g(ctx->device);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return cuda_status(counted(ctx, VIT_K_RMSNORM, st, [&] {
+    return launch_rmsnorm(ctx->cfg.dtype == VIT_F32 ? kF32 : kBF16, x, residual, gamma, h, y, rows,
+                          cols, eps, st);
+  }));
+}
+
+vit_status vit_rmsnorm_mx8(vit_ctx *ctx, const void *x, const void *residual, const void *gamma,
+                           void *h, int rows, int cols, float eps, void *codes, void *scales,
+                           void *stream) {
+  if (!ctx || !x || !gamma || !codes || !scales) return VIT_ERR_INVALID_ARG;
+  if (ctx->cfg.dtype != VIT_BF16) return VIT_ERR_UNSUPPORTED;
+  const vit_status s = check_rmsnorm(ctx, x, residual, gamma, h, nullptr, rows, cols, eps);
+  if (s != VIT_OK) return s;
+  if (!aligned16(codes) || !aligned16(scales)) return VIT_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return VIT_OK;
+  const size_t n = size_t(rows) * cols * 2, nc = size_t(rows) * mx8_row_bytes(cols),
+               ns = mx8_scale_bytes(rows, cols);
+  const void *ps[4] = {x, residual, h, gamma};
+  for (int i = 0; i < 4; ++i) {
+    const size_t np = i < 3 ? n : size_t(cols) * 2;
+    if (overlap(codes, nc, ps[i], np) || overlap(scales, ns, ps[i], np)) return VIT_ERR_INVALID_ARG;
+  }
+  if (overlap(codes, nc, scales, ns)) return VIT_ERR_INVALID_ARG;
+  DeviceGuard g(ctx->device);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return cuda_status(counted(ctx, VIT_K_RMSNORM, st, [&] {
+    return launch_rmsnorm_mx8(x, residual, gamma, h, rows, cols, eps,
+                              static_cast<uint8_t *>(codes), static_cast<uint8_t *>(scales), st);
+  }));
+}
+
+// ---------------------------------------------------------------- MXFP4
+size_t vit_mx4_row_bytes(int K) { return K < 0 ? 0 : mx4_row_bytes(K); }
+size_t vit_mx4_scale_bytes(int rows, int K) {
+  return rows < 0 || K < 0 ? 0 : mx4_scale_bytes(rows, K);
+}
+
+namespace {
+
+// Column counts up to here keep the kernels' 32-bit column arithmetic.
+constexpr int kMaxMx4Cols = 1 << 30;
+
+vit_status check_mx4_matrix(const vit_ctx *ctx, const void *x, const void *codes,
+                            const void *scales, int rows, int K) {
+  if (!ctx || !x || !codes || !scales || rows < 0 || K < 0) return VIT_ERR_INVALID_ARG;
+  if (ctx->cfg.dtype != VIT_BF16 || K > kMaxMx4Cols) return VIT_ERR_UNSUPPORTED;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return VIT_ERR_INVALID_ARG;
+  const size_t n = size_t(rows) * K * 2, nc = size_t(rows) * mx4_row_bytes(K),
+               ns = mx4_scale_bytes(rows, K);
+  return overlap(x, n, codes, nc) || overlap(x, n, scales, ns) || overlap(codes, nc, scales, ns)
+             ? VIT_ERR_INVALID_ARG
+             : VIT_OK;
+}
+
+}  // namespace
+
+vit_status vit_mx4_quantize(vit_ctx *ctx, const void *x, int rows, int K, void *codes,
+                            void *scales, void *stream) {
+  const vit_status s = check_mx4_matrix(ctx, x, codes, scales, rows, K);
+  if (s != VIT_OK || rows == 0 || K == 0) return s;
+  DeviceGuard g(ctx->device);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return cuda_status(counted(ctx, VIT_K_MX4_QUANTIZE, st, [&] {
+    return launch_mx4_quantize(x, rows, K, static_cast<uint8_t *>(codes),
+                               static_cast<uint8_t *>(scales), st);
+  }));
+}
+
+vit_status vit_mx4_dequantize(vit_ctx *ctx, const void *codes, const void *scales, int rows, int K,
+                              void *y, void *stream) {
+  const vit_status s = check_mx4_matrix(ctx, y, codes, scales, rows, K);
+  if (s != VIT_OK || rows == 0 || K == 0) return s;
+  DeviceGuard g(ctx->device);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return cuda_status(counted(ctx, VIT_K_MX4_QUANTIZE, st, [&] {
+    return launch_mx4_dequantize(static_cast<const uint8_t *>(codes),
+                                 static_cast<const uint8_t *>(scales), rows, K, y, st);
+  }));
+}
+
+vit_status vit_linear_mx4(vit_ctx *ctx, const void *a_codes, const void *a_scales,
+                          const void *w_codes, const void *w_scales, const void *bias,
+                          const void *residual, void *y, int M, int N, int K, vit_epilogue epi,
+                          void *stream) {
+  if (!ctx || !a_codes || !a_scales || !w_codes || !w_scales || !y || M < 0 || N <= 0 || K <= 0)
+    return VIT_ERR_INVALID_ARG;
+  if (epi != VIT_EPI_BIAS && epi != VIT_EPI_BIAS_GELU && epi != VIT_EPI_BIAS_RESIDUAL)
+    return VIT_ERR_INVALID_ARG;
+  if (epi == VIT_EPI_BIAS_RESIDUAL && !residual) return VIT_ERR_INVALID_ARG;
+  if (ctx->cfg.dtype != VIT_BF16 || N % 8 || K > kMaxMx4Cols) return VIT_ERR_UNSUPPORTED;
+  const void *ps[7] = {a_codes, a_scales, w_codes, w_scales, bias, residual, y};
+  for (const void *p : ps)
+    if (p && !aligned16(p)) return VIT_ERR_INVALID_ARG;
+  if (M == 0) return VIT_OK;
+  const size_t ny = size_t(M) * N * 2;
+  if (overlap(y, ny, a_codes, size_t(M) * mx4_row_bytes(K)) ||
+      overlap(y, ny, a_scales, mx4_scale_bytes(M, K)) ||
+      overlap(y, ny, w_codes, size_t(N) * mx4_row_bytes(K)) ||
+      overlap(y, ny, w_scales, mx4_scale_bytes(N, K)) || overlap(y, ny, bias, size_t(N) * 2) ||
+      (epi == VIT_EPI_BIAS_RESIDUAL && residual != y && overlap(y, ny, residual, ny)))
+    return VIT_ERR_INVALID_ARG;
+  DeviceGuard g(ctx->device);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return cuda_status(counted(ctx, VIT_K_GEMM_MX4, st, [&] {
+    return launch_gemm_mx4(static_cast<const uint8_t *>(a_codes),
+                           static_cast<const uint8_t *>(a_scales),
+                           static_cast<const uint8_t *>(w_codes),
+                           static_cast<const uint8_t *>(w_scales), bias,
+                           epi == VIT_EPI_BIAS_RESIDUAL ? residual : nullptr, y, M, N, K, int(epi),
+                           ctx->num_sms, ctx->d_status, st);
+  }));
+}
+
+// ---------------------------------------------------------------- three-axis RoPE
+namespace {
+
+// The pairs of a head of d dims, and the width of the runs of consecutive dims
+// they come in (a power of two).
+int rope3d_table(Rope3dTable &t, int d, const int32_t *sec, vit_rope_layout layout, float theta) {
+  const int half = d / 2;
+  auto set = [&](int p, int lo, int hi, int axis, double exponent) {
+    const double turns = fmod(pow(double(theta), -exponent) / (2 * acos(-1.0)), 1.0);
+    t.lo[p] = uint8_t(lo);
+    t.hi[p] = uint8_t(hi);
+    t.axis[p] = uint8_t(axis);
+    t.turn[p] = uint64_t(ldexp(turns, 64));
+  };
+  unsigned runs = unsigned(half);
+  if (layout == VIT_ROPE_BLOCKS) {
+    int p = 0;
+    for (int a = 0; a < 3; ++a) {
+      for (int j = 0; j < sec[a]; ++j)
+        set(p + j, 2 * p + j, 2 * p + sec[a] + j, a, double(j) / sec[a]);
+      p += sec[a];
+      runs |= unsigned(sec[a]);
+    }
+  } else {
+    int left[3] = {sec[0], sec[1], sec[2]}, a = 0;
+    for (int p = 0; p < half; ++p) {
+      while (left[a] == 0) a = (a + 1) % 3;
+      set(p, p, p + half, a, 2.0 * p / d);
+      --left[a];
+      if (layout == VIT_ROPE_TURNS) a = (a + 1) % 3;
+    }
+  }
+  return int(runs & (~runs + 1u));
+}
+
+// Whether an element of the rows y (width w, stride ys) may be one of the rows
+// x (width w, stride xs), both of `rows` rows; strides and width in elements.
+bool rows_overlap(const char *x, long long xs, const char *y, long long ys, long long w, int rows,
+                  size_t es) {
+  const size_t nx = (size_t(rows - 1) * xs + w) * es, ny = (size_t(rows - 1) * ys + w) * es;
+  if (!overlap(x, nx, y, ny)) return false;
+  if (xs != ys) return true;
+  const long long delta = y - x, pitch = xs * (long long)es, width = w * (long long)es;
+  const long long r = ((delta % pitch) + pitch) % pitch;  // of one row's start in the other's rows
+  return r < width || r > pitch - width;
+}
+
+}  // namespace
+
+vit_status vit_rope3d(vit_ctx *ctx, const void *x, long long x_stride, void *y, long long y_stride,
+                      const int32_t *pos_thw, int total_tokens, int heads,
+                      const int32_t *sections_host, vit_rope_layout layout, void *stream) {
+  if (!ctx || !x || !y || !pos_thw || !sections_host || total_tokens < 0 || heads < 1)
+    return VIT_ERR_INVALID_ARG;
+  if (layout != VIT_ROPE_BLOCKS && layout != VIT_ROPE_SECTIONS && layout != VIT_ROPE_TURNS)
+    return VIT_ERR_INVALID_ARG;
+  const vit_config &c = ctx->cfg;
+  const int32_t *sec = sections_host;
+  if (sec[0] < 0 || sec[1] < 0 || sec[2] < 0) return VIT_ERR_INVALID_ARG;
+  if ((long long)sec[0] + sec[1] + sec[2] != c.head_dim / 2) return VIT_ERR_SHAPE;
+  const long long width = (long long)heads * c.head_dim;
+  if (x_stride < width || y_stride < width) return VIT_ERR_SHAPE;
+  const size_t es = esize(c);
+  if (reinterpret_cast<uintptr_t>(x) % es || reinterpret_cast<uintptr_t>(y) % es ||
+      reinterpret_cast<uintptr_t>(pos_thw) % 4)
+    return VIT_ERR_INVALID_ARG;
+  if (total_tokens == 0) return VIT_OK;
+  // offsets in bytes stay far inside 64 bits
+  if (x_stride > (1ll << 30) || y_stride > (1ll << 30)) return VIT_ERR_UNSUPPORTED;
+  const bool in_place = x == y && x_stride == y_stride;
+  if (!in_place && rows_overlap(static_cast<const char *>(x), x_stride, static_cast<char *>(y),
+                                y_stride, width, total_tokens, es))
+    return VIT_ERR_INVALID_ARG;
+  if (overlap(pos_thw, size_t(total_tokens) * 12, y,
+              (size_t(total_tokens - 1) * y_stride + width) * es))
+    return VIT_ERR_INVALID_ARG;
+  Rope3dTable tab{};
+  const int run = rope3d_table(tab, c.head_dim, sec, layout, c.rope_theta);
+  DeviceGuard g(ctx->device);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return cuda_status(counted(ctx, VIT_K_ROPE, st, [&] {
+    return launch_rope3d(c.dtype == VIT_F32 ? kF32 : kBF16, x, x_stride, y, y_stride, pos_thw,
+                         total_tokens, heads, c.head_dim, tab, run, st);
+  }));
 }
 
 vit_status vit_rope2d(vit_ctx *ctx, void *qkv, const int32_t *pos_rc, int total_tokens,
