@@ -139,6 +139,17 @@ def test_linear(ctx, M, N, K, epi):
     check_linear(ctx, M, N, K, epi, M + N + K, bias=(M + K) % 3 != 0)
 
 
+@pytest.mark.parametrize("tile", ["1x128", "2x128", "2x192", "2x256"])
+@pytest.mark.parametrize("M,N,K,epi", [
+    (1, 8, 65, 2), (129, 392, 130, 1), (255, 200, 640, 2), (300, 1152, 1100, 0), (700, 1160, 2049, 2),
+    (1300, 4304, 300, 1), (5000, 2056, 257, 2)])
+def test_linear_every_tile(ctx, monkeypatch, tile, M, N, K, epi):
+    """Every tile shape on sizes that the choice by size gives to another: odd
+    rows and columns, one to several tiles a worker."""
+    monkeypatch.setenv("VIT_MX4_TILE", tile)
+    check_linear(ctx, M, N, K, epi, M + N + K)
+
+
 @pytest.mark.parametrize("M,N,K,epi", [(3900, 4304, 1152, 1), (3900, 3456, 1152, 0),
                                        (10936, 1152, 4304, 2), (960, 1152, 1152, 2)])
 def test_linear_layer_sizes(ctx, M, N, K, epi):

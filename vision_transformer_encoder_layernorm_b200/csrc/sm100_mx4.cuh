@@ -60,6 +60,13 @@ __device__ __forceinline__ void tmem_cp_scales(uint32_t dst_tmem, uint64_t src_d
                  : "memory");
 }
 
+// Asks for [p, p + bytes) to be brought into L2 (16-byte aligned, a multiple of 16).
+__device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(p)),
+               "r"(bytes)
+               : "memory");
+}
+
 // 3-D tiled bulk tensor copy global -> shared, completion on an mbarrier of
 // this CTA, or (PAIR) on one of the pair's leader at a cluster address.
 template <bool PAIR>
