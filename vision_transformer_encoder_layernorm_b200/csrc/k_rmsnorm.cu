@@ -7,18 +7,20 @@
 // bf16 element, 7 with MXFP8 codes); the row stays in registers between the
 // sum of squares and the output.
 //
-// Numerics.  The squares are summed in fp64 (one conversion and one DFMA an
-// element, far below the fp64 rate at this bandwidth), so neither large rows
-// overflow nor long ones lose bits, and a bf16 output is the correctly rounded
-// value of the formula for the stored h: the product h gamma is exact in fp32
-// (8 + 8 significant bits), times fp32 1/rms it is within 2 ulp, and the few
-// values that close to a bf16 rounding border are recomputed in fp64.  The
-// MXFP8 codes are those of the bf16 output (mx8_quantize_kernel's rule), so
-// they do not depend on how the sum is split over threads either.
+// Numerics.  The squares are summed in fp64, so neither large rows overflow nor
+// long ones lose bits, and a bf16 output is the correctly rounded value of the
+// formula for the stored h.  h gamma is exact in fp32 (8 + 8 significant bits);
+// times fp32 1/rms it is within 2 ulp, and a vector with a value that close to
+// a bf16 border is redone with the product's rounding error and the second half
+// of 1/rms.  The MXFP8 codes are those of the bf16 output (mx8_quantize_kernel's
+// rule), so they do not depend on how the sum is split over threads either.
+// fp64 costs little here: a bf16 value becomes an fp64 one by moving its bits (a
+// conversion instruction an element cost 1.3 us on 3900 x 1152 rows).
 #include <cuda_fp8.h>
 
 #include "kernels.h"
 #include "mx8.h"
+#include "sm100.cuh"
 
 namespace vit {
 
@@ -37,6 +39,17 @@ struct RowVec<__nv_bfloat16> {
     return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
                       pack_bf16x2(f[6], f[7]));
   }
+  // rounded once: for two bf16 values that is what rounding their fp32 sum gives
+  // (where that sum is inexact one of them is below 2^-16 of the other, far from
+  // moving it by half a step)
+  static __device__ __forceinline__ uint32_t add2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 s = __hadd2_rn(*reinterpret_cast<const __nv_bfloat162 *>(&a),
+                                        *reinterpret_cast<const __nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&s);
+  }
+  static __device__ __forceinline__ uint4 add(const uint4 &a, const uint4 &b) {
+    return make_uint4(add2(a.x, b.x), add2(a.y, b.y), add2(a.z, b.z), add2(a.w, b.w));
+  }
 };
 template <>
 struct RowVec<float> {
@@ -49,11 +62,19 @@ struct RowVec<float> {
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
                       __float_as_uint(f[3]));
   }
+  static __device__ __forceinline__ uint4 add(const uint4 &a, const uint4 &b) {
+    float u[4], v[4];
+    unpack(a, u);
+    unpack(b, v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) u[e] += v[e];
+    return pack(u);
+  }
 };
 
 // An fp32 value that rounds to the same bf16 as v does: v rounded to fp32,
 // moved off a bf16 midpoint to the side v lies on.
-__device__ __noinline__ float bf16_side(double v) {
+__device__ __forceinline__ float bf16_side(double v) {
   const float f = __double2float_rn(v);
   uint32_t u = __float_as_uint(f);
   if ((u & 0xFFFFu) == 0x8000u) {
@@ -64,82 +85,153 @@ __device__ __noinline__ float bf16_side(double v) {
   return __uint_as_float(u);
 }
 
-// TPR threads per row (a divisor of the block), thread t holding the 16-byte
-// vectors t, t + TPR, ... (V at most).  MX8: y goes out as codes and scales;
-// four neighbouring threads hold a 32-column group, sixteen the 128 columns
-// whose four scale bytes make one word of the scale blocks.  The MX8 grid
-// covers the padded rows of the last block row, whose scale bytes are 127.
-// x, res, h and y may be the same buffers row by row: a thread reads its
-// vectors before it writes them, and no other thread touches them.
-template <typename T, bool MX8, int TPR, int V>
-__global__ void __launch_bounds__(TPR > 256 ? TPR : 256)
+// h gamma rstd of 8 bf16 columns, correctly rounded, for rows and values whose
+// fp32 products might leave the normal range.  Out of line: rarely taken, and
+// inlined its registers halve the occupancy.
+__device__ __noinline__ uint4 exact8(uint4 h, uint4 gamma, double rstd) {
+  float a[8], g[8], o[8];
+  RowVec<__nv_bfloat16>::unpack(h, a);
+  RowVec<__nv_bfloat16>::unpack(gamma, g);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) o[e] = bf16_side(double(a[e]) * double(g[e]) * rstd);
+  return RowVec<__nv_bfloat16>::pack(o);
+}
+
+// p (rh + rl), rounded to fp32 and moved off a bf16 midpoint to its own side; p
+// exact, the product's error recovered by fused multiply-add.
+__device__ __forceinline__ float bf16_side2(float p, float rh, float rl) {
+  const float hi = p * rh;
+  const float err = fmaf(p, rl, fmaf(p, rh, -hi));
+  const float s = hi + err, rest = err - (s - hi);
+  uint32_t u = __float_as_uint(s);
+  if ((u & 0xFFFFu) == 0x8000u && rest != 0.f) u += (rest > 0.f) == (s > 0.f) ? 1u : ~0u;
+  return __uint_as_float(u);
+}
+
+// Sum of squares of 16 bytes of a row.
+template <typename T>
+__device__ __noinline__ double exact_squares(uint4 v) {
+  float a[RowVec<T>::N];
+  RowVec<T>::unpack(v, a);
+  double s = 0.0;
+#pragma unroll
+  for (int e = 0; e < RowVec<T>::N; ++e) s = fma(double(a[e]), double(a[e]), s);
+  return s;
+}
+
+// The same of a thread's vectors, times kSquareScale.  A normal bf16 value's
+// magnitude times 2^128 is an fp64 one with its bits moved and one exponent bit
+// set; what that makes of zeros and subnormals (below 2^-126) and of infinities
+// and NaN (2^128 and up) the caller sees by the size of the row's sum, and asks
+// for exact_squares.
+template <typename T>
+constexpr double kSquareScale = sizeof(T) == 2 ? 0x1p256 : 1.0;
+template <typename T, int V>
+__device__ __forceinline__ double moved_squares(const uint4 (&hv)[V]) {
+  double part[4] = {};  // four chains
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const uint32_t w[4] = {hv[i].x, hv[i].y, hv[i].z, hv[i].w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if constexpr (sizeof(T) == 2) {
+        const double lo = __hiloint2double(int(((w[q] << 13) & 0x0FFFE000u) | 0x40000000u), 0);
+        const double hi = __hiloint2double(int(((w[q] >> 3) & 0x0FFFE000u) | 0x40000000u), 0);
+        part[(2 * q) & 3] = fma(lo, lo, part[(2 * q) & 3]);
+        part[(2 * q + 1) & 3] = fma(hi, hi, part[(2 * q + 1) & 3]);
+      } else {
+        const double a = double(__uint_as_float(w[q]));
+        part[q] = fma(a, a, part[q]);
+      }
+    }
+  }
+  return (part[0] + part[1]) + (part[2] + part[3]);
+}
+
+// 1 / sqrt(v): fp32's, and one Newton step in fp64 (its error squared, 2^-44);
+// the library's where v leaves the fp32 range.
+__device__ __forceinline__ double inverse_root(double v) {
+  if (!(v > 0x1p-100 && v < 0x1p100)) return rsqrt(v);
+  const double r = double(rsqrtf(float(v)));
+  return fma(0.5 * r, fma(-v * r, r, 1.0), r);
+}
+
+// A row takes blockDim.x threads (whole warps), thread t holding the 16-byte
+// vectors t, t + blockDim.x, ... (V at most); blockDim.y rows a block.  MX8: y
+// goes out as codes and scales; four neighbouring threads hold a 32-column group,
+// sixteen the 128 columns whose four scale bytes make one word of the scale
+// blocks.  The MX8 grid covers the padded rows of the last block row, whose scale
+// bytes are 127.  x, res, h and y may be the same buffers row by row: a thread
+// reads its vectors before it writes them, and no other thread touches them.
+template <typename T, bool MX8, int V>
+__global__ void __launch_bounds__(V == 5 ? 512 : 1024, V == 5 ? 2 : 1)
     rmsnorm_kernel(const T *x, const T *res, const T *__restrict__ gamma, T *h, T *y, int rows,
-                   int cols, float eps, uint8_t *__restrict__ codes, uint8_t *__restrict__ scales,
-                   size_t row_bytes, int k_blocks) {
+                   int cols, double inv_cols, float eps, uint8_t *__restrict__ codes,
+                   uint8_t *__restrict__ scales, size_t row_bytes, int k_blocks) {
   using R = RowVec<T>;
   constexpr int N = R::N;
-  constexpr int kThreads = TPR > 256 ? TPR : 256;
-  __shared__ double red[kThreads / 32];
+  __shared__ double red[32];
   pdl_trigger();
   pdl_wait();
-  const int t = threadIdx.x % TPR, lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR;
+  const int t = threadIdx.x, tpr = blockDim.x, lane = t & 31, row_warps = tpr >> 5;
+  const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
   const bool active = row < rows;
   const int nvec = cols / N;
   const size_t base = size_t(active ? row : 0) * nvec;
   const uint4 *xr = reinterpret_cast<const uint4 *>(x) + base;
   const uint4 *rr = reinterpret_cast<const uint4 *>(res) + base;
-  uint4 hv[V];
+  uint4 hv[V], rv[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int c = t + TPR * i;
-    hv[i] = active && c < nvec ? xr[c] : make_uint4(0, 0, 0, 0);
+    const int c = t + tpr * i;
+    hv[i] = rv[i] = make_uint4(0, 0, 0, 0);
+    if (active && c < nvec) {
+      hv[i] = xr[c];
+      if (res != nullptr) rv[i] = rr[c];
+    }
   }
   if (res != nullptr) {
-    uint4 rv[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = t + TPR * i;
-      rv[i] = active && c < nvec ? rr[c] : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      float a[N], b[N];
-      R::unpack(hv[i], a);
-      R::unpack(rv[i], b);
-#pragma unroll
-      for (int e = 0; e < N; ++e) a[e] += b[e];
-      hv[i] = R::pack(a);
+      hv[i] = R::add(hv[i], rv[i]);
     }
   }
   if (h != nullptr && active) {
     uint4 *hr = reinterpret_cast<uint4 *>(h) + base;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = t + TPR * i;
+      const int c = t + tpr * i;
       if (c < nvec) hr[c] = hv[i];
     }
   }
-  double ss = 0.0;
+  double ss, mean;
+  for (int pass = 0;; ++pass) {
+    if (pass == 0) {
+      ss = moved_squares<T, V>(hv);
+    } else {
+      ss = 0.0;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    float a[N];
-    R::unpack(hv[i], a);
+      for (int i = 0; i < V; ++i) ss += exact_squares<T>(hv[i]);
+    }
 #pragma unroll
-    for (int e = 0; e < N; ++e) ss = fma(double(a[e]), double(a[e]), ss);
+    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (row_warps > 1) {
+      const int w0 = threadIdx.y * row_warps;
+      if (lane == 0) red[w0 + (t >> 5)] = ss;
+      __syncthreads();
+      ss = 0.0;
+      for (int w = 0; w < row_warps; ++w) ss += red[w0 + w];
+    }
+    mean = ss * (pass == 0 ? inv_cols * (1.0 / kSquareScale<T>) : inv_cols);
+    if (sizeof(T) == 4 || pass > 0) break;
+    // moved bits stand for the values where the sum is between these (padding
+    // and zeros count 2^-254 each); a block's rows go together
+    const bool fine = ss > kSquareScale<T> * 0x1p-180 && ss < kSquareScale<T> * 0x1p250;
+    if (row_warps > 1 ? __syncthreads_and(fine) : fine) break;
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  if constexpr (TPR > 32) {
-    if (lane == 0) red[threadIdx.x >> 5] = ss;
-    __syncthreads();
-    const int w0 = threadIdx.x / TPR * (TPR / 32);
-    ss = 0.0;
-#pragma unroll
-    for (int w = 0; w < TPR / 32; ++w) ss += red[w0 + w];
-  }
-  const double rstd = rsqrt(ss / double(cols) + double(eps));
-  const float rh = float(rstd);
+  const double rstd = inverse_root(mean + double(eps));
+  const float rh = float(rstd), rl = float(rstd - double(rh));
+  const uint64_t rh2 = f2_pack(rh, rh);
   // rows so large or small that h gamma might leave the fp32 range (and a row
   // of zeros without eps, or one with an infinity or NaN) take fp64 throughout
   const bool wide = !(rh > 0x1p-100f && rh < 0x1p100f);
@@ -152,37 +244,46 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256)
   uint4 *yr = reinterpret_cast<uint4 *>(y) + base;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int c = t + TPR * i;
+    const int c = t + tpr * i;
     if (MX8 ? (c & ~15) * N >= k_blocks * 128 : c >= nvec) break;
     const bool ok = active && c < nvec;
+    const uint4 gv = ok ? __ldg(gr + c) : make_uint4(0, 0, 0, 0);
     float a[N], g[N], o[N];
     R::unpack(hv[i], a);
-    R::unpack(ok ? __ldg(gr + c) : make_uint4(0, 0, 0, 0), g);
+    R::unpack(gv, g);
+    uint4 packed;
     if constexpr (N == 8) {
-      bool near = wide;
+      // o is less than 2 ulp off (1/rms and the product are rounded): only one
+      // that is within 1 ulp of a bf16 midpoint may round to another bf16 than
+      // the formula's value
+      // (tested on the low halves of two values a word; the upper may take the
+      // lower one's carry)
+      uint32_t least = 0xFFFFFFFFu;
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        o[e] = (a[e] * g[e]) * rh;
-        near |= ((__float_as_uint(o[e]) - 0x7FFDu) & 0xFFFFu) <= 6u;  // 3 ulp about a midpoint
+      for (int e = 0; e < N; e += 2) {
+        const uint64_t p = f2_mul(f2_pack(a[e], a[e + 1]), f2_pack(g[e], g[e + 1]));  // exact
+        f2_unpack(p, a[e], a[e + 1]);
+        f2_unpack(f2_mul(p, rh2), o[e], o[e + 1]);
+        least = __vminu2(least, __byte_perm(__float_as_uint(o[e]), __float_as_uint(o[e + 1]),
+                                            0x5410) + 0x80018001u);
       }
+      const bool near = wide || min(least & 0xFFFFu, least >> 16) <= 3u;
+      packed = R::pack(o);
       if (near) {
-#pragma unroll 1
+        bool small = wide;
+#pragma unroll
         for (int e = 0; e < N; ++e) {
-          float v = 0.f;  // o[e] by a runtime index would spill the arrays
-#pragma unroll
-          for (int q = 0; q < N; ++q)
-            if (q == e) v = bf16_side(double(a[q]) * double(g[q]) * rstd);
-#pragma unroll
-          for (int q = 0; q < N; ++q)
-            if (q == e) o[q] = v;
+          small |= o[e] != 0.f && fabsf(o[e]) < 0x1p-90f;  // the error terms would be subnormal
+          o[e] = bf16_side2(a[e], rh, rl);
         }
+        packed = small ? exact8(hv[i], gv, rstd) : R::pack(o);
       }
     } else {
 #pragma unroll
       for (int e = 0; e < N; ++e)
         o[e] = wide ? float(double(a[e]) * double(g[e]) * rstd) : (a[e] * rh) * g[e];
+      packed = R::pack(o);
     }
-    const uint4 packed = R::pack(o);
     if constexpr (!MX8) {
       yr[c] = packed;
     } else {
@@ -223,34 +324,39 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256)
   }
 }
 
-template <typename T, bool MX8, int TPR, int V>
+template <typename T, bool MX8, int V>
 cudaError_t run(const void *x, const void *res, const void *gamma, void *h, void *y, int rows,
-                int cols, float eps, uint8_t *codes, uint8_t *scales, cudaStream_t st) {
-  constexpr int threads = TPR > 256 ? TPR : 256;
+                int cols, float eps, uint8_t *codes, uint8_t *scales, int nvec, cudaStream_t st) {
+  const int tpr = ((nvec + V - 1) / V + 31) / 32 * 32;
+  const int rpb = std::max(1, 256 / tpr);  // rows of a block
   const long long all = MX8 ? ((long long)rows + 127) / 128 * 128 : rows;
-  const long long grid = (all + threads / TPR - 1) / (threads / TPR);
-  return launch_pdl(rmsnorm_kernel<T, MX8, TPR, V>, dim3(unsigned(grid)), dim3(threads), 0, st, 1,
+  const long long grid = (all + rpb - 1) / rpb;
+  return launch_pdl(rmsnorm_kernel<T, MX8, V>, dim3(unsigned(grid)), dim3(tpr, rpb), 0, st, 1,
                     static_cast<const T *>(x), static_cast<const T *>(res),
                     static_cast<const T *>(gamma), static_cast<T *>(h), static_cast<T *>(y), rows,
-                    cols, eps, codes, scales, MX8 ? mx8_row_bytes(cols) : size_t(0),
+                    cols, 1.0 / cols, eps, codes, scales, MX8 ? mx8_row_bytes(cols) : size_t(0),
                     (cols + 127) / 128);
 }
 
-// Threads per row by the row's vectors: a warp up to 160 (1280 bf16 columns),
-// then 128 and 512 threads, so that a thread holds at most 5 (8 for the
-// widest rows) and has all its loads in flight at once.
+// Vectors a thread holds.  With few rows, one (the fewest a block of 1024 threads
+// allows): each thread's code is short (1 row of 1152 columns 1.9 us, with five
+// 3.0).  Where the rows need more threads than the SMs hold at once, five: the
+// row's reduction and its root are then shared by more columns (10936 x 1152: 19.9
+// us, with one 31.0).
 template <typename T, bool MX8>
 cudaError_t pick(const void *x, const void *res, const void *gamma, void *h, void *y, int rows,
-                 int cols, float eps, uint8_t *codes, uint8_t *scales, cudaStream_t st) {
+                 int cols, float eps, uint8_t *codes, uint8_t *scales, int num_sms,
+                 cudaStream_t st) {
   // MX8 threads also cover the padding columns of the last 128-column block
   const int nvec = MX8 ? (cols + 127) / 128 * 16 : cols / RowVec<T>::N;
-#define VIT_RMS(TPR, V) return run<T, MX8, TPR, V>(x, res, gamma, h, y, rows, cols, eps, codes, scales, st)
-  if (nvec <= 64) VIT_RMS(32, 2);
-  if (nvec <= 160) VIT_RMS(32, 5);
-  if (nvec <= 384) VIT_RMS(128, 3);
-  if (nvec <= 640) VIT_RMS(128, 5);
-  if (nvec <= 2048) VIT_RMS(512, 4);
-  if constexpr (RowVec<T>::N == 4) VIT_RMS(512, 8);
+#define VIT_RMS(V) return run<T, MX8, V>(x, res, gamma, h, y, rows, cols, eps, codes, scales, nvec, st)
+  const bool many = sizeof(T) == 2 && (long long)rows * nvec > 1024ll * num_sms;
+  if (many && nvec > 64 && nvec <= 2560) VIT_RMS(5);
+  if (many && nvec <= 64) VIT_RMS(2);
+  if (nvec <= 1024) VIT_RMS(1);
+  if (nvec <= 2048) VIT_RMS(2);
+  if constexpr (RowVec<T>::N == 4)
+    if (nvec <= 4096) VIT_RMS(4);
 #undef VIT_RMS
   return cudaErrorInvalidValue;
 }
@@ -258,16 +364,18 @@ cudaError_t pick(const void *x, const void *res, const void *gamma, void *h, voi
 }  // namespace
 
 cudaError_t launch_rmsnorm(int dtype, const void *x, const void *res, const void *gamma, void *h,
-                           void *y, int rows, int cols, float eps, cudaStream_t st) {
-  return dtype == kF32
-             ? pick<float, false>(x, res, gamma, h, y, rows, cols, eps, nullptr, nullptr, st)
-             : pick<__nv_bfloat16, false>(x, res, gamma, h, y, rows, cols, eps, nullptr, nullptr, st);
+                           void *y, int rows, int cols, float eps, int num_sms, cudaStream_t st) {
+  return dtype == kF32 ? pick<float, false>(x, res, gamma, h, y, rows, cols, eps, nullptr, nullptr,
+                                            num_sms, st)
+                       : pick<__nv_bfloat16, false>(x, res, gamma, h, y, rows, cols, eps, nullptr,
+                                                    nullptr, num_sms, st);
 }
 
 cudaError_t launch_rmsnorm_mx8(const void *x, const void *res, const void *gamma, void *h, int rows,
-                               int cols, float eps, uint8_t *codes, uint8_t *scales,
+                               int cols, float eps, uint8_t *codes, uint8_t *scales, int num_sms,
                                cudaStream_t st) {
-  return pick<__nv_bfloat16, true>(x, res, gamma, h, nullptr, rows, cols, eps, codes, scales, st);
+  return pick<__nv_bfloat16, true>(x, res, gamma, h, nullptr, rows, cols, eps, codes, scales,
+                                   num_sms, st);
 }
 
 }  // namespace vit

@@ -64,9 +64,9 @@ cudaError_t launch_rope2d(int dtype, void *qkv, const int32_t *pos, int T, int H
 // multiple of 8 (bf16) or 4 (fp32), at most 16384.  The MXFP8 form writes y as
 // codes and scales (layout as launch_mx8_quantize).
 cudaError_t launch_rmsnorm(int dtype, const void *x, const void *res, const void *gamma, void *h,
-                           void *y, int rows, int cols, float eps, cudaStream_t st);
+                           void *y, int rows, int cols, float eps, int num_sms, cudaStream_t st);
 cudaError_t launch_rmsnorm_mx8(const void *x, const void *res, const void *gamma, void *h, int rows,
-                               int cols, float eps, uint8_t *codes, uint8_t *scales,
+                               int cols, float eps, uint8_t *codes, uint8_t *scales, int num_sms,
                                cudaStream_t st);
 
 // Three-axis RoPE (k_rope3d.cu).  Pair p < d/2 of a head: dims lo and hi, the

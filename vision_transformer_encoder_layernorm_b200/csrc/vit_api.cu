@@ -1095,7 +1095,7 @@ vit_status vit_rmsnorm(vit_ctx *ctx, const void *x, const void *residual, const 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return cuda_status(counted(ctx, VIT_K_RMSNORM, st, [&] {
     return launch_rmsnorm(ctx->cfg.dtype == VIT_F32 ? kF32 : kBF16, x, residual, gamma, h, y, rows,
-                          cols, eps, st);
+                          cols, eps, ctx->num_sms, st);
   }));
 }
 
@@ -1120,7 +1120,8 @@ vit_status vit_rmsnorm_mx8(vit_ctx *ctx, const void *x, const void *residual, co
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return cuda_status(counted(ctx, VIT_K_RMSNORM, st, [&] {
     return launch_rmsnorm_mx8(x, residual, gamma, h, rows, cols, eps,
-                              static_cast<uint8_t *>(codes), static_cast<uint8_t *>(scales), st);
+                              static_cast<uint8_t *>(codes), static_cast<uint8_t *>(scales),
+                              ctx->num_sms, st);
   }));
 }
 
