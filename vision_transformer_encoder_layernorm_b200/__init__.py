@@ -78,6 +78,7 @@ class VitSeqs(ctypes.Structure):
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_Int3 = ctypes.c_int32 * 3
 # name -> (restype, argtypes); the exported C ABI of include/vit.h
 ABI_FUNCTIONS = {
     "vit_init": (_I, [ctypes.POINTER(VitConfig), _I, ctypes.POINTER(_P)]),
@@ -258,32 +259,46 @@ class Context:
         self._h = h
         self._device = device
 
-    # Checks of the entry points that take tensors of a fixed layout: the C call
-    # sees bare pointers, so a wrong type, device, shape or stride is refused here.
-    def _dense(self, fn: str, t, dtype, shape):
-        """t: a contiguous tensor of this type and shape on the context's device."""
-        if t.dtype != dtype or t.get_device() != self._device or not t.is_contiguous():
+    # Checks of the entry points below that take tensors of a fixed layout: the C
+    # call sees bare pointers, so a wrong type, device, shape or stride is refused
+    # here.  They run on every call, so they ask a tensor for as little as they can.
+    def _dense(self, fn: str, shape, *tensors):
+        """Contiguous tensors (or None) of the context's element type and this
+        shape on its device."""
+        dt, dev = self._element, self._device
+        for t in tensors:
+            if t is not None:
+                if t.dtype is not dt or t.get_device() != dev or not t.is_contiguous():
+                    raise VitError(fn, 1)
+                if t.shape != shape:
+                    raise VitError(fn, 2)
+
+    def _codes(self, fn: str, codes, scales, rows: int, row_bytes: int, K: int):
+        """Contiguous byte tensors of at least the sizes of a [rows, K] matrix in
+        a microscaled format."""
+        u8, dev = self._u8, self._device
+        if (codes.dtype is not u8 or scales.dtype is not u8 or codes.get_device() != dev
+                or scales.get_device() != dev or not codes.is_contiguous()
+                or not scales.is_contiguous()):
             raise VitError(fn, 1)
-        if tuple(t.shape) != shape:
+        if (codes.numel() < rows * row_bytes
+                or scales.numel() < (rows + 127) // 128 * ((K + 127) // 128) * 512):
             raise VitError(fn, 2)
 
-    def _bytes(self, fn: str, t, size: int):
-        """t: a contiguous byte tensor of at least `size` bytes on the device."""
-        import torch
-        if t.dtype != torch.uint8 or t.get_device() != self._device or not t.is_contiguous():
-            raise VitError(fn, 1)
-        if t.numel() < size:
-            raise VitError(fn, 2)
-
-    def _element(self):
-        import torch
-        return torch.bfloat16 if self.cfg.dtype == BF16 else torch.float32
+    def __getattr__(self, name):
+        # the types to compare with, once torch is needed
+        if name in ("_element", "_u8"):
+            import torch
+            self._element = torch.bfloat16 if self.cfg.dtype == BF16 else torch.float32
+            self._u8 = torch.uint8
+            return self.__dict__[name]
+        raise AttributeError(name)
 
     def _on(self, stream):
         """The given stream, or the current one of the context's device."""
         if stream is None:
             import torch
-            return torch.cuda.current_stream(self._device).cuda_stream
+            return torch._C._cuda_getCurrentRawStream(self._device)
         return stream if isinstance(stream, int) else stream.cuda_stream
 
     @property
@@ -428,95 +443,94 @@ class Context:
                                                     _ptr(w[1]), _ptr(bias), _ptr(residual), _ptr(y),
                                                     M, N, K, epi, _stream(stream)))
 
-    def _norm_args(self, fn, x, gamma, residual, h):
-        rows, cols = x.shape
-        dt = self._element()
-        self._dense(fn, x, dt, (rows, cols))
-        self._dense(fn, gamma, dt, (cols,))
-        for t in (residual, h):
-            if t is not None:
-                self._dense(fn, t, dt, (rows, cols))
-        return rows, cols
-
     def rmsnorm(self, x, gamma, y, residual=None, h=None, eps=None, stream=None):
         """vit_rmsnorm: y = h / sqrt(mean(h^2) + eps) * gamma of h = x +
         residual (h = x without one); h, if given, receives the sum."""
-        rows, cols = self._norm_args("vit_rmsnorm", x, gamma, residual, h)
-        self._dense("vit_rmsnorm", y, x.dtype, (rows, cols))
-        e = self.cfg.ln_eps if eps is None else eps
-        _check("vit_rmsnorm", lib.vit_rmsnorm(self._h, _ptr(x), _ptr(residual), _ptr(gamma),
-                                              _ptr(h), _ptr(y), rows, cols, e, self._on(stream)))
+        rows, cols = x.shape
+        self._dense("vit_rmsnorm", (rows, cols), x, y, residual, h)
+        self._dense("vit_rmsnorm", (cols,), gamma)
+        _check("vit_rmsnorm", lib.vit_rmsnorm(
+            self._h, x.data_ptr(), None if residual is None else residual.data_ptr(),
+            gamma.data_ptr(), None if h is None else h.data_ptr(), y.data_ptr(), rows, cols,
+            self.cfg.ln_eps if eps is None else eps, self._on(stream)))
 
     def rmsnorm_mx8(self, x, gamma, codes, scales, residual=None, h=None, eps=None, stream=None):
         """vit_rmsnorm_mx8: rmsnorm straight to MXFP8 codes / scales (the layout
         of mx8_quantize)."""
-        rows, cols = self._norm_args("vit_rmsnorm_mx8", x, gamma, residual, h)
-        self._bytes("vit_rmsnorm_mx8", codes, rows * ((cols + 15) // 16 * 16))
-        self._bytes("vit_rmsnorm_mx8", scales, mx8_scale_bytes(rows, cols))
-        e = self.cfg.ln_eps if eps is None else eps
+        rows, cols = x.shape
+        self._dense("vit_rmsnorm_mx8", (rows, cols), x, residual, h)
+        self._dense("vit_rmsnorm_mx8", (cols,), gamma)
+        self._codes("vit_rmsnorm_mx8", codes, scales, rows, (cols + 15) // 16 * 16, cols)
         _check("vit_rmsnorm_mx8", lib.vit_rmsnorm_mx8(
-            self._h, _ptr(x), _ptr(residual), _ptr(gamma), _ptr(h), rows, cols, e, _ptr(codes),
-            _ptr(scales), self._on(stream)))
-
-    def _mx4_args(self, fn, pair, rows, K):
-        codes, scales = pair
-        self._bytes(fn, codes, rows * mx4_row_bytes(K))
-        self._bytes(fn, scales, mx4_scale_bytes(rows, K))
+            self._h, x.data_ptr(), None if residual is None else residual.data_ptr(),
+            gamma.data_ptr(), None if h is None else h.data_ptr(), rows, cols,
+            self.cfg.ln_eps if eps is None else eps, codes.data_ptr(), scales.data_ptr(),
+            self._on(stream)))
 
     def mx4_quantize(self, x, codes, scales, stream=None):
         """bf16 x [rows, K] -> MXFP4 codes [rows, mx4_row_bytes(K)] (uint8) and
         scales [mx4_scale_bytes(rows, K)] (uint8), see vit_mx4_quantize."""
         rows, K = x.shape
-        self._dense("vit_mx4_quantize", x, self._element(), (rows, K))
-        self._mx4_args("vit_mx4_quantize", (codes, scales), rows, K)
-        _check("vit_mx4_quantize", lib.vit_mx4_quantize(self._h, _ptr(x), rows, K, _ptr(codes),
-                                                        _ptr(scales), self._on(stream)))
+        self._dense("vit_mx4_quantize", (rows, K), x)
+        self._codes("vit_mx4_quantize", codes, scales, rows, (K + 31) // 32 * 16, K)
+        _check("vit_mx4_quantize", lib.vit_mx4_quantize(
+            self._h, x.data_ptr(), rows, K, codes.data_ptr(), scales.data_ptr(),
+            self._on(stream)))
 
     def mx4_dequantize(self, codes, scales, y, stream=None):
         """MXFP4 codes and scales of a [rows, K] matrix -> bf16 y [rows, K]."""
         rows, K = y.shape
-        self._dense("vit_mx4_dequantize", y, self._element(), (rows, K))
-        self._mx4_args("vit_mx4_dequantize", (codes, scales), rows, K)
+        self._dense("vit_mx4_dequantize", (rows, K), y)
+        self._codes("vit_mx4_dequantize", codes, scales, rows, (K + 31) // 32 * 16, K)
         _check("vit_mx4_dequantize", lib.vit_mx4_dequantize(
-            self._h, _ptr(codes), _ptr(scales), rows, K, _ptr(y), self._on(stream)))
+            self._h, codes.data_ptr(), scales.data_ptr(), rows, K, y.data_ptr(),
+            self._on(stream)))
 
     def linear_mx4(self, a, w, bias, y, K, epi=EPI_BIAS, residual=None, stream=None):
         """y = epi(deq(A) deq(W)^T + bias) with a = (codes, scales) [M, K] and
         w = (codes, scales) [N, K] from mx4_quantize."""
         fn = "vit_linear_mx4"
         M, N = y.shape
-        dt = self._element()
-        self._dense(fn, y, dt, (M, N))
-        self._mx4_args(fn, a, M, K)
-        self._mx4_args(fn, w, N, K)
-        if bias is not None:
-            self._dense(fn, bias, dt, (N,))
-        if residual is not None:
-            self._dense(fn, residual, dt, (M, N))
-        _check(fn, lib.vit_linear_mx4(self._h, _ptr(a[0]), _ptr(a[1]), _ptr(w[0]), _ptr(w[1]),
-                                      _ptr(bias), _ptr(residual), _ptr(y), M, N, K, epi,
-                                      self._on(stream)))
+        (ac, asc), (wc, wsc) = a, w
+        row_bytes = (K + 31) // 32 * 16
+        self._dense(fn, (M, N), y, residual)
+        self._dense(fn, (N,), bias)
+        self._codes(fn, ac, asc, M, row_bytes, K)
+        self._codes(fn, wc, wsc, N, row_bytes, K)
+        _check(fn, lib.vit_linear_mx4(
+            self._h, ac.data_ptr(), asc.data_ptr(), wc.data_ptr(), wsc.data_ptr(),
+            None if bias is None else bias.data_ptr(),
+            None if residual is None else residual.data_ptr(), y.data_ptr(), M, N, K, epi,
+            self._on(stream)))
 
     def rope3d(self, x, pos_thw, sections, layout=ROPE_BLOCKS, out=None, stream=None):
         """vit_rope3d on x [T, heads, head_dim] (rows of a wider tensor may be
         sliced: only the token stride is free), into ``out`` or in place."""
         import torch
         fn = "vit_rope3d"
-        T, heads, d = x.shape
+        shape = x.shape
+        T, heads, d = shape
         y = x if out is None else out
-        for t in (x, y):
-            if t.dtype != self._element() or t.get_device() != self._device:
+        dt, dev = self._element, self._device
+        strides = []
+        for t in (x,) if out is None else (x, out):
+            if t.dtype is not dt or t.get_device() != dev:
                 raise VitError(fn, 1)
-            if tuple(t.shape) != (T, heads, d) or d != self.cfg.head_dim or len(sections) != 3:
+            st = t.stride()
+            if t.shape != shape or d != self.cfg.head_dim or len(sections) != 3:
                 raise VitError(fn, 2)
-            if t.numel() and ((heads > 1 and t.stride(1) != d) or t.stride(2) != 1):
+            if T and heads and ((heads > 1 and st[1] != d) or st[2] != 1):
                 raise VitError(fn, 1)
-        self._dense(fn, pos_thw, torch.int32, (T, 3))
-        # a single token has no stride to go by
-        xs, ys = (max(t.stride(0), heads * d) if T <= 1 else t.stride(0) for t in (x, y))
-        sec = (ctypes.c_int32 * 3)(*sections)
-        _check(fn, lib.vit_rope3d(self._h, _ptr(x), xs, _ptr(y), ys, _ptr(pos_thw), T, heads, sec,
-                                  layout, self._on(stream)))
+            # a single token has no stride to go by
+            strides.append(max(st[0], heads * d) if T <= 1 else st[0])
+        if (pos_thw.dtype is not torch.int32 or pos_thw.get_device() != dev
+                or not pos_thw.is_contiguous()):
+            raise VitError(fn, 1)
+        if pos_thw.shape != (T, 3):
+            raise VitError(fn, 2)
+        _check(fn, lib.vit_rope3d(self._h, x.data_ptr(), strides[0], y.data_ptr(), strides[-1],
+                                  pos_thw.data_ptr(), T, heads, _Int3(*sections), layout,
+                                  self._on(stream)))
 
     def rope2d(self, qkv, pos_rc, stream=None):
         _check("vit_rope2d", lib.vit_rope2d(self._h, _ptr(qkv), _ptr(pos_rc), qkv.shape[0],

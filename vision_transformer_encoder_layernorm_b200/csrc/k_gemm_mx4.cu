@@ -434,21 +434,19 @@ cudaError_t run(const Args &g) {
   const bool warm = na + nw <= kPrefetchMost;
   const Prefetch pre{{g.a_codes, g.w_codes}, {warm ? na : 0, warm ? nw : 0}};
   auto kern = gemm_mx4_kernel<BN, EPI, PAIR>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(CF::kSmemBytes));
-  if (e != cudaSuccess) return e;
-  const long long tiles =
-      ((long long)g.M + kCtas * BM - 1) / (kCtas * BM) * ((g.N + BN - 1) / BN);
-  if (tiles > 0x7FFFFFFFll - 4ll * g.num_sms) return cudaErrorInvalidValue;
-  int most = g.num_sms;
-  if constexpr (PAIR) {
-    // pairs that run at once: clusters live inside a GPC, so perhaps not one per
-    // two SMs (queried once per device; concurrent first calls find the same)
-    static std::atomic<int> cached[kMaxDevices];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
-    most = dev < kMaxDevices ? cached[dev].load(std::memory_order_relaxed) : 0;
-    if (most <= 0) {
+  // asked for once per device: the kernel's shared memory and, for pairs, how
+  // many run at once (clusters live inside a GPC, so perhaps not one per two SMs;
+  // concurrent first calls find the same)
+  static std::atomic<int> cached[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+  int most = dev < kMaxDevices ? cached[dev].load(std::memory_order_acquire) : 0;
+  if (most <= 0) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               int(CF::kSmemBytes));
+    if (e != cudaSuccess) return e;
+    most = g.num_sms;
+    if constexpr (PAIR) {
       cudaLaunchAttribute attr[1];
       attr[0].id = cudaLaunchAttributeClusterDimension;
       attr[0].val.clusterDim.x = 2;
@@ -463,9 +461,12 @@ cudaError_t run(const Args &g) {
         cudaGetLastError();
         most = g.num_sms / 2;
       }
-      if (dev < kMaxDevices) cached[dev].store(most, std::memory_order_relaxed);
     }
+    if (dev < kMaxDevices) cached[dev].store(most, std::memory_order_release);
   }
+  const long long tiles =
+      ((long long)g.M + kCtas * BM - 1) / (kCtas * BM) * ((g.N + BN - 1) / BN);
+  if (tiles > 0x7FFFFFFFll - 4ll * g.num_sms) return cudaErrorInvalidValue;
   const int workers = int(std::min<long long>(tiles, most));
   return launch_pdl(kern, dim3(workers * kCtas), dim3(CF::kThreads), CF::kSmemBytes, g.st, kCtas, ta,
                     tb, sa, sb, tr, ty, g.bias, g.M, g.N, g.K, g.status, pre);
