@@ -8,36 +8,19 @@
 // decides it.
 //
 // Bound: HBM (2 bytes read, 17/32 written an element; the other way round for
-// the dequantiser).  A thread takes 8 columns at a time: 16 bytes of bf16 are
-// one word of codes, 4 threads a group (two shuffles for its maximum), 16
-// threads the 128 columns whose four scale bytes are one word.  A warp takes a
-// segment of a row, at most 1024 columns, its loads issued together; a row's
-// segments are of equal length, in 128-column blocks.
+// the dequantiser), with instructions close behind: at 6.4 TB/s an SM has about
+// 16 issue slots an element.  The quantiser gives a thread a whole group, so the
+// scale is found once for 32 elements; the dequantiser gives it 8 columns (a word
+// of codes, 16 bytes out), so that its stores are whole lines.
 #include <cuda_bf16.h>
-#include <cuda_fp4.h>
 
 #include "kernels.h"
 #include "mx4.h"
+#include "sm100.cuh"
 
 namespace vit {
 
 namespace {
-
-constexpr int kVecs = 4;  // 8-column vectors a thread holds: 1024 columns a warp
-
-// Where a warp works: its row and its 128-column blocks [kb0, kb1).
-struct Segment {
-  long long row;
-  int kb0, kb1;
-};
-__device__ __forceinline__ Segment segment_of(int k_blocks, int n_seg, int per) {
-  const long long w = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  Segment s;
-  s.row = w / n_seg;
-  s.kb0 = int(w - s.row * n_seg) * per;
-  s.kb1 = min(s.kb0 + per, k_blocks);
-  return s;
-}
 
 // 8 columns from k0 (a multiple of 8) of a row of K; zeros past K.  ALIGN:
 // elements that are sure to be aligned together at the row's start.
@@ -80,122 +63,158 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *row, int k0, int K, const 
   }
 }
 
+// Four fp32 pairs as eight E2M1 codes, the first in the low nibble.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&f)[8]) {
+  uint32_t w;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(w)
+      : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
+  return w;
+}
+
+__device__ __forceinline__ __nv_bfloat162 as_bf16x2(uint32_t v) {
+  return *reinterpret_cast<const __nv_bfloat162 *>(&v);
+}
+__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v) {
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// A block takes rows_per_block rows, a thread one 32-column group at a time of
+// their padded groups (4 per 128 columns, so that every scale byte is written).
 template <int ALIGN>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(512)
     mx4_quantize_kernel(const __nv_bfloat16 *__restrict__ x, int rows, int K, size_t row_bytes,
-                        int k_blocks, int n_seg, int per, uint8_t *__restrict__ codes,
+                        int k_blocks, int rows_per_block, uint8_t *__restrict__ codes,
                         uint8_t *__restrict__ scales) {
   pdl_trigger();
   pdl_wait();
-  const Segment s = segment_of(k_blocks, n_seg, per);
-  if (s.row >= ((long long)rows + 127) / 128 * 128) return;  // whole warps
-  const int lane = threadIdx.x & 31;
-  const bool active = s.row < rows;  // the other rows only have padding scales
-  const __nv_bfloat16 *xr = x + size_t(active ? s.row : 0) * K;
-  uint8_t *cr = codes + size_t(active ? s.row : 0) * row_bytes;
-  const int rr = int(s.row & 127);
-  uint8_t *sr = scales + size_t(s.row >> 7) * k_blocks * 512 + (rr & 31) * 16 + (rr >> 5) * 4;
-  uint4 v[kVecs];
+  const int groups = (K + 31) / 32, pgroups = 4 * k_blocks;
+  const long long row0 = (long long)blockIdx.x * rows_per_block;
+  const long long prows = ((long long)rows + 127) / 128 * 128;
+  const float inv_groups = 1.0f / float(pgroups);
+  for (int u = threadIdx.x; u < rows_per_block * pgroups; u += blockDim.x) {
+    // u / pgroups: one row, or few rows of few groups (below 2^10, exact in fp32)
+    const int lr = rows_per_block == 1 ? 0 : int((float(u) + 0.5f) * inv_groups);
+    const int j = u - lr * pgroups;
+    const long long row = row0 + lr;
+    if (row >= prows) return;
+    const int rr = int(row & 127);
+    uint8_t &scale = scales[(size_t(row >> 7) * k_blocks + (j >> 2)) * 512 + (rr & 31) * 16 +
+                            (rr >> 5) * 4 + (j & 3)];
+    if (row >= rows || j >= groups) {
+      scale = 127;
+      continue;
+    }
+    const __nv_bfloat16 *xr = x + size_t(row) * K;
+    uint4 v[4];
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    const int k0 = s.kb0 * 128 + (lane + 32 * i) * 8;
-    v[i] = active && k0 < s.kb1 * 128 ? load8<ALIGN>(xr, k0, K) : make_uint4(0, 0, 0, 0);
-  }
+    for (int i = 0; i < 4; ++i) v[i] = load8<ALIGN>(xr, j * 32 + 8 * i, K);
+    __nv_bfloat162 m = as_bf16x2(0u);  // largest magnitudes; NaN stays
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    const int k0 = s.kb0 * 128 + (lane + 32 * i) * 8;
-    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-    // magnitudes compare as integers, a NaN above all
-    uint32_t m2 = 0;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) m2 = __vmaxu2(m2, w[q] & 0x7FFF7FFFu);
-    m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, 1));
-    m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, 2));
-    const uint32_t amax = max(m2 & 0xFFFFu, m2 >> 16);
-    const int ef = int(amax >> 7);
+    for (int i = 0; i < 4; ++i) {
+      m = __hmax2_nan(m, __habs2(as_bf16x2(v[i].x)));
+      m = __hmax2_nan(m, __habs2(as_bf16x2(v[i].y)));
+      m = __hmax2_nan(m, __habs2(as_bf16x2(v[i].z)));
+      m = __hmax2_nan(m, __habs2(as_bf16x2(v[i].w)));
+    }
+    const uint32_t amax = max(as_u32(m) & 0x7FFFu, (as_u32(m) >> 16) & 0x7FFFu);
     const bool nan = amax > 0x7F80u;
-    const int byte = max(ef - 2, 0);  // X + 127
+    const int byte = max(int(amax >> 7) - 2, 0);  // X + 127
     const float inv = __uint_as_float(uint32_t(254 - byte) << 23);
-    uint32_t code = 0;
+    const uint64_t inv2 = f2_pack(inv, inv);
+    uint32_t c[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float2 f = make_float2(bf16_lo(w[q]) * inv, bf16_hi(w[q]) * inv);
-      code |= uint32_t(__nv_cvt_float2_to_fp4x2(f, __NV_E2M1, cudaRoundNearest)) << (8 * q);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      float f[8];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        f2_unpack(f2_mul(f2_pack(bf16_lo(w[q]), bf16_hi(w[q])), inv2), f[2 * q], f[2 * q + 1]);
+      c[i] = nan ? 0u : e2m1x8(f);
     }
-    if (nan) code = 0;
-    const bool in_row = active && (k0 & ~31) < K;  // the group has a column
-    uint32_t word = uint32_t(!in_row ? 127 : nan ? 255 : byte) << (8 * ((lane >> 2) & 3));
-    word |= __shfl_xor_sync(0xffffffffu, word, 4);
-    word |= __shfl_xor_sync(0xffffffffu, word, 8);
-    if (k0 < s.kb1 * 128) {
-      if (in_row) *reinterpret_cast<uint32_t *>(cr + k0 / 2) = code;
-      if ((lane & 15) == 0) *reinterpret_cast<uint32_t *>(sr + size_t(k0 >> 7) * 512) = word;
-    }
+    *reinterpret_cast<uint4 *>(codes + size_t(row) * row_bytes + j * 16) =
+        make_uint4(c[0], c[1], c[2], c[3]);
+    scale = uint8_t(nan ? 255 : byte);
   }
 }
 
-// Eight E2M1 codes (one word) as bf16 words: a magnitude's high and low byte
-// are looked up by byte permutation (codes 0..7 have bf16 bits 0000 3F00 3F80
-// 3FC0 4000 4040 4080 40C0), the sign is the nibble's top bit.
-__device__ __forceinline__ void e2m1_to_bf16(uint32_t code, uint32_t (&w)[4]) {
-#pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    const uint32_t c = p == 0 ? code & 0xFFFFu : code >> 16;
-    const uint32_t hi = __byte_perm(0x3F3F3F00u, 0x40404040u, c & 0x7777u);
-    const uint32_t lo = __byte_perm(0xC0800000u, 0xC0804000u, c & 0x7777u);
-    const uint32_t a = __byte_perm(lo, hi, 0x5140u), b = __byte_perm(lo, hi, 0x7362u);
-    w[2 * p] = a | ((c & 0x8u) << 12) | ((c & 0x80u) << 24);
-    w[2 * p + 1] = b | ((c & 0x800u) << 4) | ((c & 0x8000u) << 16);
-  }
+// Four E2M1 codes (16 bits) as two bf16 words, times s (a power of two, twice).
+// A magnitude's high and low byte are looked up by byte permutation (codes 0..7
+// have bf16 bits 0000 3F00 3F80 3FC0 4000 4040 4080 40C0).  A third permutation
+// takes the codes whole: a nibble's top bit makes it replicate the picked byte's
+// top bit, FF for a negative code and 80 for a positive one, which shifted by one
+// has the sign where the high byte wants it.
+__device__ __forceinline__ void e2m1_to_bf16(uint32_t code, __nv_bfloat162 s, uint32_t &w0,
+                                             uint32_t &w1) {
+  const uint32_t c = code & 0x7777u;
+  uint32_t sign;  // (the intrinsic ignores the selectors' top bits)
+  asm("prmt.b32 %0, %1, %1, %2;" : "=r"(sign) : "r"(0x80808080u), "r"(code));
+  const uint32_t lo = __byte_perm(0xC0800000u, 0xC0804000u, c);
+  const uint32_t hi = __byte_perm(0x3F3F3F00u, 0x40404040u, c) | ((sign << 1) & 0x80808080u);
+  w0 = as_u32(__hmul2_rn(as_bf16x2(__byte_perm(lo, hi, 0x5140u)), s));
+  w1 = as_u32(__hmul2_rn(as_bf16x2(__byte_perm(lo, hi, 0x7362u)), s));
 }
 
+// A block takes rows_per_block rows, a thread 8 columns at a time.
 template <int ALIGN>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(512)
     mx4_dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
-                          int rows, int K, size_t row_bytes, int k_blocks, int n_seg, int per,
+                          int rows, int K, size_t row_bytes, int k_blocks, int rows_per_block,
                           __nv_bfloat16 *__restrict__ y) {
   pdl_trigger();
   pdl_wait();
-  const Segment s = segment_of(k_blocks, n_seg, per);
-  if (s.row >= rows) return;
-  const int lane = threadIdx.x & 31;
-  const uint8_t *cr = codes + size_t(s.row) * row_bytes;
-  __nv_bfloat16 *yr = y + size_t(s.row) * K;
-  const int rr = int(s.row & 127);
-  const uint8_t *sr = scales + size_t(s.row >> 7) * k_blocks * 512 + (rr & 31) * 16 + (rr >> 5) * 4 +
-                      ((lane >> 2) & 3);
-  uint32_t v[kVecs], sc[kVecs];
+  const int nvec = (K + 7) / 8;
+  const long long row0 = (long long)blockIdx.x * rows_per_block;
+  const float inv_vecs = 1.0f / float(nvec);
+  const int units = rows_per_block * nvec;
+  constexpr int kBatch = 4;  // loads in flight
+  for (int u0 = threadIdx.x; u0 < units; u0 += kBatch * blockDim.x) {
+    uint32_t c[kBatch], sc[kBatch];
+    int lr[kBatch];
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    const int k0 = s.kb0 * 128 + (lane + 32 * i) * 8;
-    const bool ok = k0 < s.kb1 * 128 && k0 < K;
-    v[i] = ok ? __ldg(reinterpret_cast<const uint32_t *>(cr + k0 / 2)) : 0u;
-    sc[i] = ok ? __ldg(sr + size_t(k0 >> 7) * 512) : 0u;
-  }
+    for (int i = 0; i < kBatch; ++i) {
+      const int u = u0 + i * blockDim.x;
+      lr[i] = rows_per_block == 1 ? 0 : int((float(u) + 0.5f) * inv_vecs);  // as above
+      const int j = u - lr[i] * nvec;
+      const long long row = row0 + lr[i];
+      const int rr = int(row & 127);
+      c[i] = sc[i] = 0;
+      if (u < units && row < rows) {
+        c[i] = __ldg(reinterpret_cast<const uint32_t *>(codes + size_t(row) * row_bytes) + j);
+        sc[i] = __ldg(scales + (size_t(row >> 7) * k_blocks + (j >> 4)) * 512 + (rr & 31) * 16 +
+                      (rr >> 5) * 4 + ((j >> 2) & 3));
+      }
+    }
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    const int k0 = s.kb0 * 128 + (lane + 32 * i) * 8;
-    if (k0 >= s.kb1 * 128 || k0 >= K) break;
-    // 2^X in bf16: the byte is its exponent field (2^-127 is subnormal)
-    const uint32_t b = sc[i] == 255u ? 0x7FC0u : sc[i] == 0u ? 0x0040u : sc[i] << 7;
-    const float f = __uint_as_float(b << 16);
-    uint32_t w[4];
-    e2m1_to_bf16(v[i], w);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) w[q] = pack_bf16x2(bf16_lo(w[q]) * f, bf16_hi(w[q]) * f);
-    store8<ALIGN>(yr, k0, K, w);
+    for (int i = 0; i < kBatch; ++i) {
+      const int u = u0 + i * blockDim.x;
+      const long long row = row0 + lr[i];
+      if (u < units && row < rows) {
+        // 2^X in bf16: the byte is its exponent field (2^-127 is subnormal)
+        const uint32_t b = sc[i] == 255u ? 0x7FC0u : sc[i] == 0u ? 0x0040u : sc[i] << 7;
+        const __nv_bfloat162 s = as_bf16x2(b * 0x10001u);
+        uint32_t w[4];
+        e2m1_to_bf16(c[i], s, w[0], w[1]);
+        e2m1_to_bf16(c[i] >> 16, s, w[2], w[3]);
+        store8<ALIGN>(y + size_t(row) * K, (u - lr[i] * nvec) * 8, K, w);
+      }
+    }
   }
 }
 
-// Segments of a row: as few as hold it at 8 blocks of 128 columns each, their
-// lengths equal to a block (1152 columns: 5 and 4 blocks, not 8 and 1).
+// Rows of a block and its threads for rows of `units` thread-sized pieces: about
+// `most` pieces a block, threads in whole warps with little left over.
 struct Split {
-  int k_blocks, n_seg, per;
-  explicit Split(int K) {
-    k_blocks = (K + 127) / 128;
-    n_seg = (k_blocks + 2 * kVecs - 1) / (2 * kVecs);
-    per = (k_blocks + n_seg - 1) / n_seg;
-    n_seg = (k_blocks + per - 1) / per;
+  int rows, threads;
+  Split(int units, int most, int batch) {
+    rows = std::max(1, most / units);
+    const int all = rows * units, turns = (all + 512 * batch - 1) / (512 * batch);
+    threads = std::min(512, ((all + turns * batch - 1) / (turns * batch) + 31) / 32 * 32);
   }
 };
 
@@ -203,27 +222,24 @@ struct Split {
 
 cudaError_t launch_mx4_quantize(const void *x, int rows, int K, uint8_t *codes, uint8_t *scales,
                                 cudaStream_t st) {
-  const Split sp(K);
-  const long long warps = ((long long)rows + 127) / 128 * 128 * sp.n_seg;
-  const long long grid = (warps + 7) / 8;
-  if (grid > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+  const int k_blocks = (K + 127) / 128;
+  const Split sp(4 * k_blocks, 512, 1);
+  const long long grid = (((long long)rows + 127) / 128 * 128 + sp.rows - 1) / sp.rows;
   auto kern = K % 8 == 0 ? mx4_quantize_kernel<8>
                          : K % 2 == 0 ? mx4_quantize_kernel<2> : mx4_quantize_kernel<1>;
-  return launch_pdl(kern, dim3(unsigned(grid)), dim3(256), 0, st, 1,
-                    static_cast<const __nv_bfloat16 *>(x), rows, K, mx4_row_bytes(K), sp.k_blocks,
-                    sp.n_seg, sp.per, codes, scales);
+  return launch_pdl(kern, dim3(unsigned(grid)), dim3(sp.threads), 0, st, 1,
+                    static_cast<const __nv_bfloat16 *>(x), rows, K, mx4_row_bytes(K), k_blocks,
+                    sp.rows, codes, scales);
 }
 
 cudaError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int rows, int K,
                                   void *y, cudaStream_t st) {
-  const Split sp(K);
-  const long long grid = ((long long)rows * sp.n_seg + 7) / 8;
-  if (grid > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+  const Split sp((K + 7) / 8, 1024, 4);
+  const long long grid = ((long long)rows + sp.rows - 1) / sp.rows;
   auto kern = K % 8 == 0 ? mx4_dequantize_kernel<8>
                          : K % 2 == 0 ? mx4_dequantize_kernel<2> : mx4_dequantize_kernel<1>;
-  return launch_pdl(kern, dim3(unsigned(grid)), dim3(256), 0, st, 1, codes, scales, rows, K,
-                    mx4_row_bytes(K), sp.k_blocks, sp.n_seg, sp.per,
-                    static_cast<__nv_bfloat16 *>(y));
+  return launch_pdl(kern, dim3(unsigned(grid)), dim3(sp.threads), 0, st, 1, codes, scales, rows, K,
+                    mx4_row_bytes(K), (K + 127) / 128, sp.rows, static_cast<__nv_bfloat16 *>(y));
 }
 
 }  // namespace vit
