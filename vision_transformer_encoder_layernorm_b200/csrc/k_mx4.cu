@@ -22,6 +22,8 @@ namespace vit {
 
 namespace {
 
+constexpr int kBatch = 4;  // vectors of 8 columns a dequantising thread has in flight
+
 // 8 columns from k0 (a multiple of 8) of a row of K; zeros past K.  ALIGN:
 // elements that are sure to be aligned together at the row's start.
 template <int ALIGN>
@@ -160,49 +162,40 @@ __device__ __forceinline__ void e2m1_to_bf16(uint32_t code, __nv_bfloat162 s, ui
   w1 = as_u32(__hmul2_rn(as_bf16x2(__byte_perm(lo, hi, 0x7362u)), s));
 }
 
-// A block takes rows_per_block rows, a thread 8 columns at a time.
+// blockDim.y rows a block; a row's blockDim.x threads take 8 columns at a time,
+// four loads in flight.
 template <int ALIGN>
 __global__ void __launch_bounds__(512)
     mx4_dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
-                          int rows, int K, size_t row_bytes, int k_blocks, int rows_per_block,
+                          int rows, int K, size_t row_bytes, int k_blocks,
                           __nv_bfloat16 *__restrict__ y) {
   pdl_trigger();
   pdl_wait();
-  const int nvec = (K + 7) / 8;
-  const long long row0 = (long long)blockIdx.x * rows_per_block;
-  const float inv_vecs = 1.0f / float(nvec);
-  const int units = rows_per_block * nvec;
-  constexpr int kBatch = 4;  // loads in flight
-  for (int u0 = threadIdx.x; u0 < units; u0 += kBatch * blockDim.x) {
+  const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+  if (row >= rows) return;
+  const int nvec = (K + 7) / 8, step = blockDim.x, rr = int(row & 127);
+  const uint32_t *cr = reinterpret_cast<const uint32_t *>(codes + size_t(row) * row_bytes);
+  const uint8_t *sr = scales + size_t(row >> 7) * k_blocks * 512 + (rr & 31) * 16 + (rr >> 5) * 4;
+  __nv_bfloat16 *yr = y + size_t(row) * K;
+  for (int j0 = threadIdx.x; j0 < nvec; j0 += kBatch * step) {
     uint32_t c[kBatch], sc[kBatch];
-    int lr[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const int u = u0 + i * blockDim.x;
-      lr[i] = rows_per_block == 1 ? 0 : int((float(u) + 0.5f) * inv_vecs);  // as above
-      const int j = u - lr[i] * nvec;
-      const long long row = row0 + lr[i];
-      const int rr = int(row & 127);
-      c[i] = sc[i] = 0;
-      if (u < units && row < rows) {
-        c[i] = __ldg(reinterpret_cast<const uint32_t *>(codes + size_t(row) * row_bytes) + j);
-        sc[i] = __ldg(scales + (size_t(row >> 7) * k_blocks + (j >> 4)) * 512 + (rr & 31) * 16 +
-                      (rr >> 5) * 4 + ((j >> 2) & 3));
-      }
+      const int j = j0 + i * step;
+      c[i] = j < nvec ? __ldg(cr + j) : 0u;
+      sc[i] = j < nvec ? __ldg(sr + size_t(j >> 4) * 512 + ((j >> 2) & 3)) : 0u;
     }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const int u = u0 + i * blockDim.x;
-      const long long row = row0 + lr[i];
-      if (u < units && row < rows) {
-        // 2^X in bf16: the byte is its exponent field (2^-127 is subnormal)
-        const uint32_t b = sc[i] == 255u ? 0x7FC0u : sc[i] == 0u ? 0x0040u : sc[i] << 7;
-        const __nv_bfloat162 s = as_bf16x2(b * 0x10001u);
-        uint32_t w[4];
-        e2m1_to_bf16(c[i], s, w[0], w[1]);
-        e2m1_to_bf16(c[i] >> 16, s, w[2], w[3]);
-        store8<ALIGN>(y + size_t(row) * K, (u - lr[i] * nvec) * 8, K, w);
-      }
+      const int j = j0 + i * step;
+      if (j >= nvec) break;
+      // 2^X in bf16: the byte is its exponent field (2^-127 is subnormal)
+      const uint32_t b = sc[i] == 255u ? 0x7FC0u : sc[i] == 0u ? 0x0040u : sc[i] << 7;
+      const __nv_bfloat162 s = as_bf16x2(b * 0x10001u);
+      uint32_t w[4];
+      e2m1_to_bf16(c[i], s, w[0], w[1]);
+      e2m1_to_bf16(c[i] >> 16, s, w[2], w[3]);
+      store8<ALIGN>(yr, j * 8, K, w);
     }
   }
 }
@@ -211,10 +204,10 @@ __global__ void __launch_bounds__(512)
 // `most` pieces a block, threads in whole warps with little left over.
 struct Split {
   int rows, threads;
-  Split(int units, int most, int batch) {
+  Split(int units, int most) {
     rows = std::max(1, most / units);
-    const int all = rows * units, turns = (all + 512 * batch - 1) / (512 * batch);
-    threads = std::min(512, ((all + turns * batch - 1) / (turns * batch) + 31) / 32 * 32);
+    const int all = rows * units, turns = (all + 511) / 512;
+    threads = std::min(512, ((all + turns - 1) / turns + 31) / 32 * 32);
   }
 };
 
@@ -223,7 +216,7 @@ struct Split {
 cudaError_t launch_mx4_quantize(const void *x, int rows, int K, uint8_t *codes, uint8_t *scales,
                                 cudaStream_t st) {
   const int k_blocks = (K + 127) / 128;
-  const Split sp(4 * k_blocks, 512, 1);
+  const Split sp(4 * k_blocks, 512);
   const long long grid = (((long long)rows + 127) / 128 * 128 + sp.rows - 1) / sp.rows;
   auto kern = K % 8 == 0 ? mx4_quantize_kernel<8>
                          : K % 2 == 0 ? mx4_quantize_kernel<2> : mx4_quantize_kernel<1>;
@@ -234,12 +227,14 @@ cudaError_t launch_mx4_quantize(const void *x, int rows, int K, uint8_t *codes, 
 
 cudaError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int rows, int K,
                                   void *y, cudaStream_t st) {
-  const Split sp((K + 7) / 8, 1024, 4);
-  const long long grid = ((long long)rows + sp.rows - 1) / sp.rows;
+  // four vectors a thread, or two where that leaves a row under a warp of threads
+  const int nvec = (K + 7) / 8, per = nvec >= 32 * kBatch ? kBatch : 2;
+  const int tx = std::min(512, (nvec + per - 1) / per), ty = std::max(1, 256 / tx);
+  const long long grid = ((long long)rows + ty - 1) / ty;
   auto kern = K % 8 == 0 ? mx4_dequantize_kernel<8>
                          : K % 2 == 0 ? mx4_dequantize_kernel<2> : mx4_dequantize_kernel<1>;
-  return launch_pdl(kern, dim3(unsigned(grid)), dim3(sp.threads), 0, st, 1, codes, scales, rows, K,
-                    mx4_row_bytes(K), (K + 127) / 128, sp.rows, static_cast<__nv_bfloat16 *>(y));
+  return launch_pdl(kern, dim3(unsigned(grid)), dim3(tx, ty), 0, st, 1, codes, scales, rows, K,
+                    mx4_row_bytes(K), (K + 127) / 128, static_cast<__nv_bfloat16 *>(y));
 }
 
 }  // namespace vit

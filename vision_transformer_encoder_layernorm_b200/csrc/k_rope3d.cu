@@ -22,89 +22,95 @@ namespace vit {
 
 namespace {
 
+// VEC elements in one access of up to 16 bytes, as they are stored.
 template <typename T, int VEC>
-__device__ __forceinline__ void load_vec(const T *p, float (&f)[VEC]) {
-  if constexpr (VEC * sizeof(T) == 2) {
-    f[0] = to_f32(p[0]);
-  } else {
-    constexpr int W = VEC * int(sizeof(T)) / 4;
-    uint32_t w[W];
+struct Raw {
+  static constexpr int W = VEC * int(sizeof(T)) / 4;  // 32-bit words; 0: one bf16
+  uint32_t w[W ? W : 1];
+  __device__ __forceinline__ void load(const T *p) {
     if constexpr (W == 4) {
       const uint4 r = *reinterpret_cast<const uint4 *>(p);
       w[0] = r.x; w[1] = r.y; w[2] = r.z; w[3] = r.w;
     } else if constexpr (W == 2) {
       const uint2 r = *reinterpret_cast<const uint2 *>(p);
       w[0] = r.x; w[1] = r.y;
-    } else {
+    } else if constexpr (W == 1) {
       w[0] = *reinterpret_cast<const uint32_t *>(p);
+    } else {
+      w[0] = *reinterpret_cast<const uint16_t *>(p);
     }
-#pragma unroll
-    for (int i = 0; i < VEC; ++i)
-      f[i] = sizeof(T) == 4 ? __uint_as_float(w[i * W / VEC])
-                            : (i & 1) ? bf16_hi(w[i * W / VEC]) : bf16_lo(w[i * W / VEC]);
   }
-}
-
-template <typename T, int VEC>
-__device__ __forceinline__ void store_vec(T *p, const float (&f)[VEC]) {
-  if constexpr (VEC * sizeof(T) == 2) {
-    p[0] = from_f32<T>(f[0]);
-  } else {
-    constexpr int W = VEC * int(sizeof(T)) / 4;
-    uint32_t w[W];
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(f[i]);
-      else w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
-    }
+  __device__ __forceinline__ void store(T *p) const {
     if constexpr (W == 4) *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     else if constexpr (W == 2) *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
-    else *reinterpret_cast<uint32_t *>(p) = w[0];
+    else if constexpr (W == 1) *reinterpret_cast<uint32_t *>(p) = w[0];
+    else *reinterpret_cast<uint16_t *>(p) = uint16_t(w[0]);
   }
-}
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+    else return (i & 1) ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
+  }
+  __device__ __forceinline__ void set(const float (&f)[VEC]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) w[i] = __float_as_uint(f[i]);
+    } else if constexpr (VEC == 1) {
+      w[0] = pack_bf16x2(f[0], 0.f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC / 2; ++i) w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+    }
+  }
+};
 
 constexpr int kHeadBatch = 4;  // heads a thread has in flight
 
-// Threads of a block: (token, head group, vector of VEC pairs); thread (t, g,
-// v) takes heads g, g + groups, ...  x and y may be the same buffer: an
-// element is read and written by one thread.
+// Thread (v, g, t) takes VEC pairs of token t's heads g, g + groups, ...  x and y
+// may be the same buffer: an element is read and written by one thread.
 template <typename T, int VEC>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 3)
     rope3d_kernel(const T *x, long long xs, T *y, long long ys, const int32_t *__restrict__ pos,
-                  int tokens, int heads, int d, int groups, int tok_per_block,
-                  const __grid_constant__ Rope3dTable tab) {
+                  int tokens, int heads, int d, const __grid_constant__ Rope3dTable tab) {
   extern __shared__ float2 cs[];  // [tok_per_block][d / 2] = (cos, sin)
   pdl_trigger();
   pdl_wait();
-  const int pairs = d / 2, nv = pairs / VEC, per_tok = nv * groups;
-  const int lt = threadIdx.x / per_tok, u = threadIdx.x - lt * per_tok;
-  const int g = u / nv, p0 = (u - g * nv) * VEC;
+  // blockDim = (vectors of a head, head groups, tokens)
+  const int pairs = d / 2, groups = blockDim.y, tok_per_block = blockDim.z;
+  const int p0 = threadIdx.x * VEC, g = threadIdx.y, lt = threadIdx.z;
   const long long tok0 = (long long)blockIdx.x * tok_per_block;
   const long long t = tok0 + lt;
-  const bool active = lt < tok_per_block && t < tokens;
+  const bool active = t < tokens;
   const int lo = tab.lo[p0], hi = tab.hi[p0];
   const T *xt = x + (active ? t : 0) * xs;
   T *yt = y + (active ? t : 0) * ys;
-  float a[kHeadBatch][VEC], b[kHeadBatch][VEC];
+  Raw<T, VEC> a[kHeadBatch], b[kHeadBatch];
   auto load = [&](int h0) {
 #pragma unroll
     for (int k = 0; k < kHeadBatch; ++k) {
       const int h = h0 + k * groups;
       if (active && h < heads) {
-        load_vec<T, VEC>(xt + (long long)h * d + lo, a[k]);
-        load_vec<T, VEC>(xt + (long long)h * d + hi, b[k]);
+        a[k].load(xt + h * d + lo);
+        b[k].load(xt + h * d + hi);
       }
     }
   };
   load(g);
-  for (int i = threadIdx.x; i < tok_per_block * pairs; i += blockDim.x) {
-    const int tt = i / pairs, p = i - tt * pairs;
-    if (tok0 + tt < tokens) {
-      const long long m = pos[3 * (tok0 + tt) + tab.axis[p]];
-      const uint64_t turns = uint64_t(m) * tab.turn[p];  // modulo one turn
+  // a thread keeps to one pair, so that the table in the kernel's parameters,
+  // where a warp's 32 different entries are 32 accesses, is read once
+  const int tid = (lt * groups + g) * blockDim.x + threadIdx.x;
+  const float inv = 1.0f / float(pairs);  // quotients of small integers, exact
+  const int table_toks = int((float(blockDim.x * groups * tok_per_block) + 0.5f) * inv);
+  const int first = int((float(tid) + 0.5f) * inv), p = tid - first * pairs;
+  if (first < table_toks) {  // tokens the block fills at a time
+    const uint64_t turn = tab.turn[p];
+    const int32_t *pp = pos + 3 * tok0 + tab.axis[p];
+#pragma unroll 1
+    for (int tt = first; tt < tok_per_block; tt += table_toks) {
+      if (tok0 + tt >= tokens) break;
+      const uint64_t turns = uint64_t((long long)__ldg(pp + 3 * tt)) * turn;  // modulo one turn
       float sn, c;
       sincospif(float(int32_t(turns >> 32)) * 0x1p-31f, &sn, &c);
-      cs[i] = make_float2(c, sn);
+      cs[tt * pairs + p] = make_float2(c, sn);
     }
   }
   __syncthreads();
@@ -124,11 +130,14 @@ __global__ void __launch_bounds__(256)
         float oa[VEC], ob[VEC];
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-          oa[i] = a[k][i] * c[i] - b[k][i] * sn[i];
-          ob[i] = b[k][i] * c[i] + a[k][i] * sn[i];
+          const float p = a[k].get(i), q = b[k].get(i);
+          oa[i] = p * c[i] - q * sn[i];
+          ob[i] = q * c[i] + p * sn[i];
         }
-        store_vec<T, VEC>(yt + (long long)h * d + lo, oa);
-        store_vec<T, VEC>(yt + (long long)h * d + hi, ob);
+        a[k].set(oa);
+        b[k].set(ob);
+        a[k].store(yt + h * d + lo);
+        b[k].store(yt + h * d + hi);
       }
     }
     h0 += kHeadBatch * groups;
@@ -143,12 +152,11 @@ cudaError_t run(const void *x, long long xs, void *y, long long ys, const int32_
   const int nv = d / 2 / VEC;
   // four heads a thread where the block's 256 threads allow it
   const int groups = std::max(1, std::min((heads + kHeadBatch - 1) / kHeadBatch, 256 / nv));
-  const int tpb = std::max(1, 256 / (nv * groups));
-  const int threads = (tpb * nv * groups + 31) / 32 * 32;
+  const int tpb = std::min(64, std::max(1, 256 / (nv * groups)));  // 64: the most a block's z takes
   const long long blocks = ((long long)tokens + tpb - 1) / tpb;
-  return launch_pdl(rope3d_kernel<T, VEC>, dim3(unsigned(blocks)), dim3(threads),
+  return launch_pdl(rope3d_kernel<T, VEC>, dim3(unsigned(blocks)), dim3(nv, groups, tpb),
                     sizeof(float2) * tpb * (d / 2), st, 1, static_cast<const T *>(x), xs,
-                    static_cast<T *>(y), ys, pos, tokens, heads, d, groups, tpb, tab);
+                    static_cast<T *>(y), ys, pos, tokens, heads, d, tab);
 }
 
 }  // namespace
