@@ -150,6 +150,17 @@ def test_linear_every_tile(ctx, monkeypatch, tile, M, N, K, epi):
     check_linear(ctx, M, N, K, epi, M + N + K)
 
 
+@pytest.mark.parametrize("tile", ["1x128x2", "1x128x4", "1x128x8"])
+@pytest.mark.parametrize("M,N,K,epi", [(1, 1152, 4304, 0), (1, 8, 2100, 1), (33, 136, 2049, 2),
+                                       (128, 1152, 4400, 1), (260, 264, 2305, 2)])
+def test_linear_split_tiles(ctx, monkeypatch, tile, M, N, K, epi):
+    """A tile's k-blocks over 2, 4 or 8 CTAs, in runs of unequal length."""
+    monkeypatch.setenv("VIT_MX4_TILE", tile)
+    y = check_linear(ctx, M, N, K, epi, M + N + K)[4].clone()
+    for _ in range(3):  # the sums' order does not depend on which CTA is done first
+        assert torch.equal(check_linear(ctx, M, N, K, epi, M + N + K)[4], y)
+
+
 @pytest.mark.parametrize("M,N,K,epi", [(3900, 4304, 1152, 1), (3900, 3456, 1152, 0),
                                        (10936, 1152, 4304, 2), (960, 1152, 1152, 2)])
 def test_linear_layer_sizes(ctx, M, N, K, epi):

@@ -10,7 +10,15 @@
 // block-scaled MMAs.  MMA k reads bytes 2 (k & 1) and 2 (k & 1) + 1 of each
 // row's scale word of the 128-column half k / 2.  MMAs that start past K are
 // left out: their scale half need not exist.  Two accumulators let the
-// epilogue of a tile overlap the next tile's main loop.
+// epilogue of a tile overlap the next tile's main loop.  Where tiles are few and K
+// is long, gemm_mx4_split_kernel spreads a tile's k-blocks over a cluster.
+//
+// Bound: an SM's share of the work is small at these sizes (3900 x 4304 x 1152 is
+// 3.7 tiles of 256 x 256 a pair, 0.3 us of MMA each), so no single unit is: with
+// the stores, the loads or the MMAs left out the 15.3 us become 13.9, 14.8 and
+// 14.6.  The start (first operands from DRAM, 1.3 us), the drain of the last tile's
+// stores (1.6 us) and GELU's hardware tanh (one in 16 a clock and SM) remain.  At
+// 8192 x 4096 x 8192 the tensor core is: 5570 TFLOP/s, 3.3 times cuBLAS's bf16 rate.
 //
 // PAIR: a cluster of two CTAs computes 256-row tiles (cta_group::2, M = 256):
 // each loads its own 128 rows of A, half of the tile's W rows, the scales of
@@ -116,6 +124,38 @@ __device__ __forceinline__ uint4 finish8(const uint32_t *r, const float4 *b, con
     o[e] = pack_bf16x2(lo, hi);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// One k-block of MMAs from a ring stage: scales to TMEM, then up to four K = 64
+// MMAs (`left`: columns of K from here on).  sfb_n: the TMEM columns by which the
+// tile's first W row lies inside its first scale block.
+template <int BN, bool PAIR>
+__device__ __forceinline__ void issue_k_block(uint32_t stage, uint32_t d_tmem, uint32_t sfa_t,
+                                              uint32_t sfb_t, uint32_t sfb_n, int left,
+                                              bool first) {
+  using CF = Cfg<BN, PAIR>;
+  const uint32_t sb = stage + kATileBytes, ssf = stage + CF::kSfOff;
+  const int mmas = min(4, (left + 63) / 64);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {  // 128-column halves
+    if (2 * j >= mmas) break;
+    tmem_cp_scales<PAIR>(sfa_t + 4 * j, smem_desc(ssf + 512 * j, 0, 128, 0));
+#pragma unroll
+    for (int i = 0; i < CF::kSfbBlocks; ++i)
+      tmem_cp_scales<PAIR>(sfb_t + 4 * (j * CF::kSfbBlocks + i),
+                           smem_desc(ssf + kSfBytes * (1 + i) + 512 * j, 0, 128, 0));
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (k >= mmas) break;
+    const uint64_t ad = smem_desc(stage + k * 32, 16, 1024, 2);
+    const uint64_t bd = smem_desc(sb + k * 32, 16, 1024, 2);
+    const int j = k >> 1, sf = 2 * (k & 1);
+    mma_mx4_ss<PAIR>(d_tmem, ad, bd, idesc_mx4(PAIR ? 2 * BM : BM, BN, sf),
+                     (sfa_t + 4 * j) | (uint32_t(sf) << 30),
+                     (sfb_t + sfb_n + 4 * j * CF::kSfbBlocks) | (uint32_t(sf) << 30),
+                     !first || k > 0);
+  }
 }
 
 // The codes of A and W, for the L2 prefetch at a kernel's start (bytes; 0: none).
@@ -265,34 +305,12 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::kThreads), 1)
         const uint32_t d_tmem = tmem + (a ? CF::kAcc1 : 0u);
         // a tile of 192 columns may start in the middle of a 128-row scale block:
         // its first 64 rows there are two of the block's four TMEM columns
-        const uint32_t sfb_n = sfb_t + uint32_t(tile / num_m * BN % 128 / 32);
+        const uint32_t sfb_n = uint32_t(tile / num_m * BN % 128 / 32);
         for (int kb = 0; kb < k_blocks; ++kb) {
           if (!mbar_wait(&bars->full[stage], phase, abort_flag)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + size_t(stage) * CF::kStageBytes);
-          const uint32_t sb = sa + kATileBytes;
-          const uint32_t ssf = sa + CF::kSfOff;
-          const int mmas = min(4, (K - kb * kBK + 63) / 64);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {  // 128-column halves
-            if (2 * j >= mmas) break;
-            tmem_cp_scales<PAIR>(sfa_t + 4 * j, smem_desc(ssf + 512 * j, 0, 128, 0));
-#pragma unroll
-            for (int i = 0; i < CF::kSfbBlocks; ++i)
-              tmem_cp_scales<PAIR>(sfb_t + 4 * (j * CF::kSfbBlocks + i),
-                                   smem_desc(ssf + kSfBytes * (1 + i) + 512 * j, 0, 128, 0));
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (k >= mmas) break;
-            const uint64_t ad = smem_desc(sa + k * 32, 16, 1024, 2);
-            const uint64_t bd = smem_desc(sb + k * 32, 16, 1024, 2);
-            const int j = k >> 1, sf = 2 * (k & 1);
-            mma_mx4_ss<PAIR>(d_tmem, ad, bd, idesc_mx4(kRows, BN, sf),
-                             (sfa_t + 4 * j) | (uint32_t(sf) << 30),
-                             (sfb_n + 4 * j * CF::kSfbBlocks) | (uint32_t(sf) << 30),
-                             (kb | k) != 0);
-          }
+          issue_k_block<BN, PAIR>(smem_u32(smem + size_t(stage) * CF::kStageBytes), d_tmem, sfa_t,
+                                  sfb_t, sfb_n, K - kb * kBK, kb == 0);
           any_mma = true;
           commit(&bars->empty[stage]);
           if (++stage == CF::kStages) { stage = 0; phase ^= 1; }
@@ -395,6 +413,170 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::kThreads), 1)
   if (threadIdx.x == 0 && bars->abort_flag) report_status(status, kDevTimeout);
 }
 
+// Few tiles and a long K: a cluster of SPLIT CTAs shares one 128 x 128 tile, each
+// over its own run of k-blocks.  Every CTA leaves its partial sums (the rows that
+// exist, fp32) in its shared memory, where the operand ring was; then CTA r
+// finishes columns [r, r + 1) 128 / SPLIT, adding the partials of all CTAs in
+// rank order over the cluster's shared memory, so the result does not depend on
+// which CTA is done first.  No CTA is persistent: the grid is one cluster a tile.
+template <int EPI, int SPLIT>
+__global__ void __launch_bounds__((Cfg<128, false>::kThreads), 1)
+    gemm_mx4_split_kernel(const __grid_constant__ CUtensorMap tmA,
+                          const __grid_constant__ CUtensorMap tmB,
+                          const __grid_constant__ CUtensorMap tmSa,
+                          const __grid_constant__ CUtensorMap tmSb,
+                          const __nv_bfloat16 *__restrict__ bias, const __nv_bfloat16 *res,
+                          __nv_bfloat16 *y, int M, int N, int K, int *status) {
+  constexpr int BN = 128;
+  using CF = Cfg<BN, false>;
+  constexpr int kPitch = BN + 4;  // floats of a partial row: lanes on different banks
+  static_assert(size_t(CF::kStages) * CF::kStageBytes >= size_t(BM) * kPitch * 4, "partial sums");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~uintptr_t(1023));
+  Bars *bars = reinterpret_cast<Bars *>(smem + size_t(CF::kStages) * CF::kStageBytes);
+  volatile int *abort_flag = &bars->abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = int(cluster_cta_rank()), tile = blockIdx.x / SPLIT;
+  const int num_m = (M + BM - 1) / BM, mb = tile % num_m, nb = tile / num_m;
+  const int k_blocks = (K + kBK - 1) / kBK;
+  const int kb0 = k_blocks * rank / SPLIT, kb1 = k_blocks * (rank + 1) / SPLIT;  // not empty
+
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < CF::kStages; ++s) {
+      mbar_init(&bars->full[s], 1);
+      mbar_init(&bars->empty[s], 1);
+    }
+    mbar_init(&bars->acc_full[0], 1);
+    mbar_init(&bars->drain, 1);
+    bars->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmSa);
+    tma_prefetch_desc(&tmSb);
+  }
+  if (warp == 1) {
+    tmem_alloc(&bars->tmem_base, CF::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  pdl_wait();
+
+  const int rows = min(BM, M - mb * BM);
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (elect_one()) {
+      int stage = 0;
+      uint32_t phase = 0, issued_mask = 0, issued_parity = 0;
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait(&bars->empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
+        uint8_t *sa = smem + size_t(stage) * CF::kStageBytes;
+        const uint32_t full = smem_u32(&bars->full[stage]);
+        mbar_arrive_expect_tx(&bars->full[stage], CF::kStageBytes);
+        tma_load_2d(sa, &tmA, &bars->full[stage], kb * (kBK / 2), mb * BM);
+        tma_load_2d(sa + kATileBytes, &tmB, &bars->full[stage], kb * (kBK / 2), nb * BN);
+        tma_load_3d<false>(sa + CF::kSfOff, &tmSa, full, 0, 2 * kb, mb);
+        tma_load_3d<false>(sa + CF::kSfOff + kSfBytes, &tmSb, full, 0, 2 * kb, nb);
+        issued_mask |= 1u << stage;
+        issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+        if (++stage == CF::kStages) { stage = 0; phase ^= 1; }
+      }
+      if (!ok)
+        for (int s = 0; s < CF::kStages; ++s)
+          if (issued_mask & (1u << s)) gemm::drain_wait(&bars->full[s], (issued_parity >> s) & 1);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (elect_one()) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true, any_mma = false;
+      const uint32_t sfa_t = tmem + CF::kSfaCol, sfb_t = tmem + CF::kSfbCol;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait(&bars->full[stage], phase, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        issue_k_block<BN, false>(smem_u32(smem + size_t(stage) * CF::kStageBytes), tmem, sfa_t,
+                                 sfb_t, 0, K - kb * kBK, kb == kb0);
+        any_mma = true;
+        mma_commit(&bars->empty[stage]);
+        if (++stage == CF::kStages) { stage = 0; phase ^= 1; }
+      }
+      if (ok) {
+        mma_commit(&bars->acc_full[0]);
+      } else if (any_mma) {
+        mma_commit(&bars->drain);
+        gemm::drain_wait(&bars->drain, 0);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ partial sums
+    const int ew = warp - 2, quarter = warp & 3, cg = (ew >> 2) * kCols;
+    const int row = quarter * 32 + lane;
+    if (__all_sync(0xffffffffu, mbar_wait(&bars->acc_full[0], 0, abort_flag)) &&
+        quarter * 32 < rows) {
+      tc_fence_after();
+      uint32_t r[kCols];
+      tmem_ld_cols<kCols>(tmem + (uint32_t(quarter * 32) << 16) + cg, r);
+      tmem_ld_wait();
+      if (row < rows) {
+        uint4 *p = reinterpret_cast<uint4 *>(smem) + (row * kPitch + cg) / 4;
+#pragma unroll
+        for (int u = 0; u < kCols / 4; ++u)
+          p[u] = make_uint4(r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]);
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync_all();  // every CTA's partial sums are in place
+  if (!*abort_flag) {
+    constexpr int kUnits = BN / SPLIT / 8;  // 8-column pieces of this CTA's columns
+    const uint32_t base = smem_u32(smem);
+    for (int u = threadIdx.x; u < rows * kUnits; u += CF::kThreads) {
+      const int row = u / kUnits, c = rank * (BN / SPLIT) + u % kUnits * 8;
+      const int col = nb * BN + c;
+      if (col >= N) continue;
+      const size_t at = size_t(mb * BM + row) * N + col;
+      const uint4 rv = EPI == kEpiResidual ? __ldcg(reinterpret_cast<const uint4 *>(res + at))
+                                           : make_uint4(0, 0, 0, 0);
+      const uint4 b4 = bias != nullptr ? __ldg(reinterpret_cast<const uint4 *>(bias + col))
+                                       : make_uint4(0, 0, 0, 0);
+      const float4 b[2] = {make_float4(bf16_lo(b4.x), bf16_hi(b4.x), bf16_lo(b4.y), bf16_hi(b4.y)),
+                           make_float4(bf16_lo(b4.z), bf16_hi(b4.z), bf16_lo(b4.w), bf16_hi(b4.w))};
+      float4 s[SPLIT][2];
+#pragma unroll
+      for (int q = 0; q < SPLIT; ++q)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          s[q][e] = ld_cluster(map_addr_to_cta(base + uint32_t(row * kPitch + c + 4 * e) * 4, q));
+      float v[8] = {};
+#pragma unroll
+      for (int q = 0; q < SPLIT; ++q) {
+        v[0] += s[q][0].x; v[1] += s[q][0].y; v[2] += s[q][0].z; v[3] += s[q][0].w;
+        v[4] += s[q][1].x; v[5] += s[q][1].y; v[6] += s[q][1].z; v[7] += s[q][1].w;
+      }
+      uint32_t r[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r[e] = __float_as_uint(v[e]);
+      *reinterpret_cast<uint4 *>(y + at) = finish8<EPI>(r, b, rv);
+    }
+  }
+  cluster_sync_all();  // no CTA leaves while another may read its partial sums
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, CF::kTmemCols);
+  }
+  if (threadIdx.x == 0 && bars->abort_flag) report_status(status, kDevTimeout);
+}
+
 struct Args {
   const uint8_t *a_codes, *a_scales, *w_codes, *w_scales;
   const __nv_bfloat16 *bias, *res;
@@ -406,12 +588,11 @@ struct Args {
 
 // Codes as [rows, bytes] with 128-byte boxes, scales as [block rows][k blocks]
 // [512 bytes] with boxes of two k blocks, residual and output in 32 x 64 boxes.
-template <int BN, int EPI, bool PAIR>
-cudaError_t run(const Args &g) {
-  using CF = Cfg<BN, PAIR>;
-  constexpr int kCtas = PAIR ? 2 : 1;
+struct Maps {
+  CUtensorMap a, b, sa, sb, res, y;
+};
+bool encode_maps(Maps &m, const Args &g, int b_rows, int sb_blocks, bool residual) {
   const uint64_t kb = (uint64_t(g.K) + 127) / 128, bytes = (uint64_t(g.K) + 1) / 2;
-  CUtensorMap ta, tb, sa, sb, tr, ty;
   auto codes = [&](CUtensorMap *t, const uint8_t *p, int rows, int box) {
     return encode_tensor_map_2d(t, CU_TENSOR_MAP_DATA_TYPE_UINT8, p, bytes, rows,
                                 mx4_row_bytes(g.K), kBK / 2, box, CU_TENSOR_MAP_SWIZZLE_128B);
@@ -425,11 +606,28 @@ cudaError_t run(const Args &g) {
     return encode_tensor_map_2d(t, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, g.N, g.M,
                                 uint64_t(g.N) * 2, kCols, 32, CU_TENSOR_MAP_SWIZZLE_128B);
   };
-  if (codes(&ta, g.a_codes, g.M, BM) || codes(&tb, g.w_codes, g.N, CF::kBRows) ||
-      scales(&sa, g.a_scales, g.M, 1) || scales(&sb, g.w_scales, g.N, CF::kSfbBlocks) ||
-      chunks(&ty, g.y) || (EPI == kEpiResidual && chunks(&tr, g.res)))
+  if (codes(&m.a, g.a_codes, g.M, BM) || codes(&m.b, g.w_codes, g.N, b_rows) ||
+      scales(&m.sa, g.a_scales, g.M, 1) || scales(&m.sb, g.w_scales, g.N, sb_blocks) ||
+      chunks(&m.y, g.y) || (residual && chunks(&m.res, g.res)))
+    return false;
+  if (!residual) m.res = m.y;  // not read
+  return true;
+}
+
+// The device's cache slot of a kernel's launch size, or null.
+std::atomic<int> *launch_slot(std::atomic<int> *slots) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
+  return &slots[dev < kMaxDevices ? dev : kMaxDevices];
+}
+
+template <int BN, int EPI, bool PAIR>
+cudaError_t run(const Args &g) {
+  using CF = Cfg<BN, PAIR>;
+  constexpr int kCtas = PAIR ? 2 : 1;
+  Maps m;
+  if (!encode_maps(m, g, CF::kBRows, CF::kSfbBlocks, EPI == kEpiResidual))
     return cudaErrorInvalidValue;
-  if (EPI != kEpiResidual) tr = ty;  // not read
   const size_t na = size_t(g.M) * mx4_row_bytes(g.K), nw = size_t(g.N) * mx4_row_bytes(g.K);
   const bool warm = na + nw <= kPrefetchMost;
   const Prefetch pre{{g.a_codes, g.w_codes}, {warm ? na : 0, warm ? nw : 0}};
@@ -437,10 +635,10 @@ cudaError_t run(const Args &g) {
   // asked for once per device: the kernel's shared memory and, for pairs, how
   // many run at once (clusters live inside a GPC, so perhaps not one per two SMs;
   // concurrent first calls find the same)
-  static std::atomic<int> cached[kMaxDevices];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
-  int most = dev < kMaxDevices ? cached[dev].load(std::memory_order_acquire) : 0;
+  static std::atomic<int> slots[kMaxDevices + 1];
+  std::atomic<int> *slot = launch_slot(slots);
+  if (slot == nullptr) return cudaErrorInvalidDevice;
+  int most = slot < slots + kMaxDevices ? slot->load(std::memory_order_acquire) : 0;
   if (most <= 0) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                int(CF::kSmemBytes));
@@ -462,14 +660,43 @@ cudaError_t run(const Args &g) {
         most = g.num_sms / 2;
       }
     }
-    if (dev < kMaxDevices) cached[dev].store(most, std::memory_order_release);
+    slot->store(most, std::memory_order_release);
   }
   const long long tiles =
       ((long long)g.M + kCtas * BM - 1) / (kCtas * BM) * ((g.N + BN - 1) / BN);
   if (tiles > 0x7FFFFFFFll - 4ll * g.num_sms) return cudaErrorInvalidValue;
   const int workers = int(std::min<long long>(tiles, most));
-  return launch_pdl(kern, dim3(workers * kCtas), dim3(CF::kThreads), CF::kSmemBytes, g.st, kCtas, ta,
-                    tb, sa, sb, tr, ty, g.bias, g.M, g.N, g.K, g.status, pre);
+  return launch_pdl(kern, dim3(workers * kCtas), dim3(CF::kThreads), CF::kSmemBytes, g.st, kCtas, m.a,
+                    m.b, m.sa, m.sb, m.res, m.y, g.bias, g.M, g.N, g.K, g.status, pre);
+}
+
+template <int EPI, int SPLIT>
+cudaError_t run_split(const Args &g) {
+  using CF = Cfg<128, false>;
+  Maps m;
+  if (!encode_maps(m, g, 128, 1, false)) return cudaErrorInvalidValue;
+  auto kern = gemm_mx4_split_kernel<EPI, SPLIT>;
+  static std::atomic<int> slots[kMaxDevices + 1];
+  std::atomic<int> *slot = launch_slot(slots);
+  if (slot == nullptr) return cudaErrorInvalidDevice;
+  if (slot == slots + kMaxDevices || slot->load(std::memory_order_acquire) == 0) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               int(CF::kSmemBytes));
+    if (e != cudaSuccess) return e;
+    slot->store(1, std::memory_order_release);
+  }
+  const int tiles = (g.M + BM - 1) / BM * ((g.N + 127) / 128);  // at most the SMs
+  return launch_pdl(kern, dim3(tiles * SPLIT), dim3(CF::kThreads), CF::kSmemBytes, g.st, SPLIT,
+                    m.a, m.b, m.sa, m.sb, g.bias, g.res, g.y, g.M, g.N, g.K, g.status);
+}
+
+template <int SPLIT>
+cudaError_t run_split_epi(const Args &g, int epi) {
+  switch (epi) {
+    case kEpiGelu: return run_split<kEpiGelu, SPLIT>(g);
+    case kEpiResidual: return run_split<kEpiResidual, SPLIT>(g);
+    default: return run_split<kEpiBias, SPLIT>(g);
+  }
 }
 
 template <int BN, bool PAIR>
@@ -485,38 +712,51 @@ cudaError_t run_epi(const Args &g, int epi) {
 // {1152, 3456, 4304} x {1152, 4304}, 960 x 4304 x 1152, 10936 x 1152 x 4304 and
 // 8192 x 4096 x 8192: a round over the SMs takes a tile's k-blocks or its
 // epilogue, whichever is longer (accumulators that share columns add a wait);
-// the first round's k-blocks and the last one's epilogue are not overlapped,
-// and a pair starts later.  One CTA wins with few k-blocks and tiles (960 x 4304
+// the first round's k-blocks and the last one's epilogue are not overlapped, a
+// pair starts later, and joining a split tile takes time by its rows and parts.  One CTA wins with few k-blocks and tiles (960 x 4304
 // x 1152: 6.8 us, pairs 7.6 to 8.5; 3900 x 1152 x 1152: 9.0 against 9.3), 192
 // columns for the wide projections (3900 x 4304 x 1152: 15.4, 128 columns 17.5,
 // 256 16.0, one CTA 18.3), 256 for the most work per byte (10936 x 1152 x 4304:
-// 35.4 against 42.0 at 128; 8192 x 4096 x 8192: 99 against 122).
+// 35.4 against 42.0 at 128; 8192 x 4096 x 8192: 99 against 122), split tiles for few
+// rows over a long K (1 x 1152 x 4304: 7.8, over 8 CTAs 4.1; 64 rows: 9.0, over 4
+// CTAs 7.3, over 8 8.6; 1 x 3456 x 1152: 3.7 either way).
 struct Shape {
-  int ctas, bn;
+  int ctas, bn, split;
   float kblock, epilogue, wait, start;
 };
-constexpr Shape kShapes[] = {{1, 128, 0.33f, 1.4f, 0.0f, 0.0f},
-                             {2, 128, 0.29f, 1.4f, 0.0f, 0.7f},
-                             {2, 192, 0.36f, 1.5f, 0.0f, 0.7f},
-                             {2, 256, 0.45f, 2.0f, 0.5f, 0.7f}};
+constexpr Shape kShapes[] = {{1, 128, 1, 0.33f, 1.4f, 0.0f, 0.0f},
+                             {1, 128, 2, 0.33f, 1.4f, 0.0f, 0.6f},
+                             {1, 128, 4, 0.33f, 1.4f, 0.0f, 0.6f},
+                             {1, 128, 8, 0.33f, 1.4f, 0.0f, 0.6f},
+                             {2, 128, 1, 0.29f, 1.4f, 0.0f, 0.7f},
+                             {2, 192, 1, 0.36f, 1.5f, 0.0f, 0.7f},
+                             {2, 256, 1, 0.45f, 2.0f, 0.5f, 0.7f}};
 
 const Shape &choose(int M, int N, int K, int num_sms) {
   const Shape *best = nullptr;
   float least = 0.f;
+  const int k_blocks = (K + kBK - 1) / kBK;
+  auto tiles_of = [&](const Shape &s) {
+    return ((long long)M + s.ctas * BM - 1) / (s.ctas * BM) * ((N + s.bn - 1) / s.bn);
+  };
+  // a split tile's CTAs run at once, and each has a k-block
+  auto fits = [&](const Shape &s) {
+    return s.split == 1 || (s.split <= k_blocks && tiles_of(s) * s.split <= num_sms);
+  };
   if (const char *f = getenv("VIT_MX4_TILE")) {  // e.g. "2x192": tuning and tests
-    int c = 0, n = 0;
-    if (sscanf(f, "%dx%d", &c, &n) == 2)
+    int c = 0, n = 0, k = 1;
+    if (sscanf(f, "%dx%dx%d", &c, &n, &k) >= 2)
       for (const Shape &s : kShapes)
-        if (s.ctas == c && s.bn == n) return s;
+        if (s.ctas == c && s.bn == n && s.split == k && fits(s)) return s;
   }
-  const float kb = float((K + kBK - 1) / kBK);
   for (const Shape &s : kShapes) {
-    if (s.ctas == 2 && M <= BM) continue;  // one row of tiles: nothing to share
-    const long long tiles =
-        ((long long)M + s.ctas * BM - 1) / (s.ctas * BM) * ((N + s.bn - 1) / s.bn);
+    if ((s.ctas == 2 && M <= BM) || !fits(s)) continue;  // one row of tiles: nothing to share
+    const long long tiles = tiles_of(s);
+    const float kb = float((k_blocks + s.split - 1) / s.split);
     const long long rounds = (tiles + num_sms / s.ctas - 1) / (num_sms / s.ctas);
     const float main = kb * s.kblock, period = std::max(main + s.wait, s.epilogue);
-    const float cost = s.start + main + float(rounds - 1) * period + s.epilogue;
+    const float join = s.split > 1 ? 0.0072f * float(std::min(M, BM) * s.split) : 0.f;
+    const float cost = s.start + main + float(rounds - 1) * period + s.epilogue + join;
     if (best == nullptr || cost < least) {
       best = &s;
       least = cost;
@@ -534,6 +774,9 @@ cudaError_t launch_gemm_mx4(const uint8_t *a_codes, const uint8_t *a_scales, con
                static_cast<const __nv_bfloat16 *>(res), static_cast<__nv_bfloat16 *>(y),
                M, N, K, num_sms, status, st};
   const Shape &s = choose(M, N, K, num_sms);
+  if (s.split == 2) return run_split_epi<2>(g, epi);
+  if (s.split == 4) return run_split_epi<4>(g, epi);
+  if (s.split == 8) return run_split_epi<8>(g, epi);
   if (s.ctas == 1) return run_epi<128, false>(g, epi);
   if (s.bn == 128) return run_epi<128, true>(g, epi);
   return s.bn == 192 ? run_epi<192, true>(g, epi) : run_epi<256, true>(g, epi);

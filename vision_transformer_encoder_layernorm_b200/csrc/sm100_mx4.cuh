@@ -67,6 +67,22 @@ __device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes) {
                : "memory");
 }
 
+// The address of `addr`, a shared-memory address of this CTA, in the CTA of rank
+// `cta` of the cluster, and 16 bytes from such an address.
+__device__ __forceinline__ uint32_t map_addr_to_cta(uint32_t addr, uint32_t cta) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(cta));
+  return r;
+}
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
 // 3-D tiled bulk tensor copy global -> shared, completion on an mbarrier of
 // this CTA, or (PAIR) on one of the pair's leader at a cluster address.
 template <bool PAIR>
