@@ -49,7 +49,8 @@ def quantize(ctx, x):
 
 
 @pytest.mark.parametrize("rows,K", [(1, 1), (1, 31), (3, 33), (5, 48), (130, 130), (257, 200),
-                                    (300, 1152), (129, 1151), (66, 4304), (7, 1025), (2, 9000)])
+                                    (300, 1152), (129, 1151), (66, 4304), (7, 1025), (2, 9000),
+                                    (17, 1154), (40, 1026), (9, 4301), (300, 35), (50, 4303)])
 def test_quantize_and_dequantize(ctx, rows, K):
     g = np.random.Generator(np.random.PCG64(rows + K))
     a = g.standard_normal((rows, K)) * np.exp2(g.integers(-30, 30, (rows, 1)))

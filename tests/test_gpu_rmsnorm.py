@@ -61,7 +61,8 @@ def summed(x, r):
 
 
 SHAPES = [(1, 8), (1, 1152), (5, 200), (129, 512), (257, 1152), (300, 1280), (33, 1288), (70, 3080),
-          (12, 4608), (9, 5128), (3, 16384), (2, 8192)]
+          (12, 4608), (9, 5128), (3, 16384), (2, 8192),
+          (3000, 1152), (3000, 64), (700, 4616), (600, 16384)]
 
 
 @pytest.mark.parametrize("residual", [False, True])
@@ -105,6 +106,44 @@ def test_rmsnorm_in_place(any_ctx):
     assert torch.equal(xx, summed(x, x))
 
 
+def test_rmsnorm_sum_of_any_bf16_values(ctx):
+    """h is the fp32 sum rounded to bf16 for every kind of pair: equal and far
+    exponents, subnormals, sums that overflow (random bit patterns, NaN left out)."""
+    g = np.random.Generator(np.random.PCG64(11))
+    bits = g.integers(0, 1 << 16, (2, 512, 4096)).astype(np.uint16)
+    near = bits[0] ^ g.integers(0, 1 << 9, bits[0].shape).astype(np.uint16)  # close in size
+    bits[1, :256] = near[:256] ^ (g.integers(0, 2, near[:256].shape).astype(np.uint16) << 15)
+    x, r = (to_dev(b, "bf16") for b in bits)
+    x[~torch.isfinite(x)], r[~torch.isfinite(r)] = 1.0, -2.0
+    h, y = torch.empty_like(x), torch.empty_like(x)
+    ctx.rmsnorm(x, torch.ones(4096, dtype=torch.bfloat16, device="cuda"), y, residual=r, h=h)
+    assert torch.equal(h.view(torch.int16), summed(x, r).view(torch.int16))
+
+
+def test_rmsnorm_rounds_correctly_next_to_borders(ctx):
+    """Many outputs within fp32 rounding of a bf16 midpoint: of twenty gammas each
+    column takes the one that brings the most of its rows there."""
+    g = np.random.Generator(np.random.PCG64(12))
+    rows, cols = 400, 1152
+    a = bf16_of(g.standard_normal((rows, cols)))
+    x = to_dev(synth.round_bf16_bits(a), "bf16")
+    best = None
+    for _ in range(20):
+        gm = bf16_of(1 + g.standard_normal(cols) * 0.3)
+        ref = NR.rmsnorm(a, gm, float(np.float32(EPS)))
+        m, _ = np.frexp(ref)
+        t = np.abs(np.abs(m) * 256 % 1 - 0.5)  # distance from a bf16 midpoint, in steps
+        score = (t < 2.0 ** -12).sum(0)
+        best = (score, gm) if best is None else (np.maximum(score, best[0]), np.where(score > best[0], gm, best[1]))
+    assert best[0].sum() > 200
+    gamma = to_dev(synth.round_bf16_bits(best[1]), "bf16")
+    ref = bf16_of(NR.rmsnorm(a, best[1], float(np.float32(EPS))))
+    for n in (3, rows):  # few rows and many rows take different thread layouts
+        y = torch.empty_like(x[:n])
+        ctx.rmsnorm(x[:n].contiguous(), gamma, y, eps=EPS)
+        assert np.array_equal(from_dev(y), ref[:n])
+
+
 def test_rmsnorm_values_at_the_ends(ctx):
     cols = 1152
     a = np.ones((6, cols))
@@ -123,7 +162,7 @@ def test_rmsnorm_values_at_the_ends(ctx):
         assert np.array_equal(from_dev(y), ref, equal_nan=True), eps
 
 
-MX_SHAPES = [(1, 8), (1, 1152), (130, 40), (257, 200), (300, 1152), (129, 1536), (20, 4608),
+MX_SHAPES = [(3900, 1152), (5000, 72), (1000, 4608), (1, 8), (1, 1152), (130, 40), (257, 200), (300, 1152), (129, 1536), (20, 4608),
              (140, 5000), (3, 16384)]
 
 

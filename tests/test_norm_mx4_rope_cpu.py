@@ -217,3 +217,15 @@ def test_binding_checks_types_shapes_and_strides(ctx):
     refused(BAD, ctx.rope3d, b(5, 72, 3).transpose(1, 2), pos, (12, 12, 12))
     refused(BAD, ctx.rope3d, b(5, 6, 72)[:, ::2], pos, (12, 12, 12))
     refused(SHAPE, ctx.rope3d, q, pos, (12, 12, 12), out=b(5, 2, 72))
+
+
+def test_binding_takes_empty_batches(ctx):
+    b = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    u = lambda *s: torch.zeros(*s, dtype=torch.uint8)     # noqa: E731
+    ctx.rmsnorm(b(0, 64), b(64), b(0, 64), residual=b(0, 64), h=b(0, 64), stream=0)
+    ctx.rmsnorm_mx8(b(0, 64), b(64), u(0, 64), u(0), stream=0)
+    ctx.mx4_quantize(b(0, 70), u(0, 48), u(0), stream=0)
+    ctx.mx4_dequantize(u(0, 48), u(0), b(0, 70), stream=0)
+    ctx.linear_mx4((u(0, 48), u(0)), (u(16, 48), u(512)), b(16), b(0, 16), 70, stream=0)
+    ctx.rope3d(b(0, 4, 72), torch.zeros(0, 3, dtype=torch.int32), (12, 12, 12), stream=0)
+    refused(SHAPE, ctx.rmsnorm, b(0, 64), b(32), b(0, 64))  # checked all the same

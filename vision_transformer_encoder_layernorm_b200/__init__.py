@@ -449,6 +449,8 @@ class Context:
         rows, cols = x.shape
         self._dense("vit_rmsnorm", (rows, cols), x, y, residual, h)
         self._dense("vit_rmsnorm", (cols,), gamma)
+        if not rows:
+            return  # an empty tensor has no address to pass
         _check("vit_rmsnorm", lib.vit_rmsnorm(
             self._h, x.data_ptr(), None if residual is None else residual.data_ptr(),
             gamma.data_ptr(), None if h is None else h.data_ptr(), y.data_ptr(), rows, cols,
@@ -461,6 +463,8 @@ class Context:
         self._dense("vit_rmsnorm_mx8", (rows, cols), x, residual, h)
         self._dense("vit_rmsnorm_mx8", (cols,), gamma)
         self._codes("vit_rmsnorm_mx8", codes, scales, rows, (cols + 15) // 16 * 16, cols)
+        if not rows:
+            return
         _check("vit_rmsnorm_mx8", lib.vit_rmsnorm_mx8(
             self._h, x.data_ptr(), None if residual is None else residual.data_ptr(),
             gamma.data_ptr(), None if h is None else h.data_ptr(), rows, cols,
@@ -473,6 +477,8 @@ class Context:
         rows, K = x.shape
         self._dense("vit_mx4_quantize", (rows, K), x)
         self._codes("vit_mx4_quantize", codes, scales, rows, (K + 31) // 32 * 16, K)
+        if not rows or not K:
+            return
         _check("vit_mx4_quantize", lib.vit_mx4_quantize(
             self._h, x.data_ptr(), rows, K, codes.data_ptr(), scales.data_ptr(),
             self._on(stream)))
@@ -482,6 +488,8 @@ class Context:
         rows, K = y.shape
         self._dense("vit_mx4_dequantize", (rows, K), y)
         self._codes("vit_mx4_dequantize", codes, scales, rows, (K + 31) // 32 * 16, K)
+        if not rows or not K:
+            return
         _check("vit_mx4_dequantize", lib.vit_mx4_dequantize(
             self._h, codes.data_ptr(), scales.data_ptr(), rows, K, y.data_ptr(),
             self._on(stream)))
@@ -497,6 +505,8 @@ class Context:
         self._dense(fn, (N,), bias)
         self._codes(fn, ac, asc, M, row_bytes, K)
         self._codes(fn, wc, wsc, N, row_bytes, K)
+        if not M:
+            return
         _check(fn, lib.vit_linear_mx4(
             self._h, ac.data_ptr(), asc.data_ptr(), wc.data_ptr(), wsc.data_ptr(),
             None if bias is None else bias.data_ptr(),
@@ -528,6 +538,8 @@ class Context:
             raise VitError(fn, 1)
         if pos_thw.shape != (T, 3):
             raise VitError(fn, 2)
+        if not T:
+            return
         _check(fn, lib.vit_rope3d(self._h, x.data_ptr(), strides[0], y.data_ptr(), strides[-1],
                                   pos_thw.data_ptr(), T, heads, _Int3(*sections), layout,
                                   self._on(stream)))

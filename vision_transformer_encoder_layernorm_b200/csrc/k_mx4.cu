@@ -24,45 +24,42 @@ namespace {
 
 constexpr int kBatch = 4;  // vectors of 8 columns a dequantising thread has in flight
 
-// 8 columns from k0 (a multiple of 8) of a row of K; zeros past K.  ALIGN:
-// elements that are sure to be aligned together at the row's start.
-template <int ALIGN>
-__device__ __forceinline__ uint4 load8(const __nv_bfloat16 *row, int k0, int K) {
-  if constexpr (ALIGN == 8) {  // K % 8 == 0: whole vectors
-    return k0 < K ? __ldg(reinterpret_cast<const uint4 *>(row + k0)) : make_uint4(0, 0, 0, 0);
-  } else {
-    uint32_t w[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int k = k0 + 2 * q;
-      if constexpr (ALIGN == 2) {
-        w[q] = k < K ? __ldg(reinterpret_cast<const uint32_t *>(row + k)) : 0u;
-      } else {
-        const unsigned short *p = reinterpret_cast<const unsigned short *>(row + k);
-        w[q] = (k < K ? uint32_t(__ldg(p)) : 0u) | (k + 1 < K ? uint32_t(__ldg(p + 1)) << 16 : 0u);
-      }
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  }
-}
+// Rows of K % 8 != 0 columns start anywhere in a 16-byte vector.  Memory is still
+// read and written in whole aligned vectors, and shifted in registers: accesses of
+// one bf16 at a time took 26 us for both ways over 3900 x 1151, against 11 for
+// 3900 x 1152.
 
-template <int ALIGN>
-__device__ __forceinline__ void store8(__nv_bfloat16 *row, int k0, int K, const uint32_t (&w)[4]) {
-  if constexpr (ALIGN == 8) {
-    if (k0 < K) *reinterpret_cast<uint4 *>(row + k0) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
+// 32 elements from element `at` of x (n elements in all, 16-byte aligned), the ones
+// past n zero.
+__device__ __forceinline__ void load_group(const __nv_bfloat16 *x, size_t at, size_t n,
+                                           uint32_t (&w)[16]) {
+  const int e = int(at & 7);
+  const uint4 *p = reinterpret_cast<const uint4 *>(x) + at / 8;
+  uint32_t a[20];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int k = k0 + 2 * q;
-      if constexpr (ALIGN == 2) {
-        if (k < K) *reinterpret_cast<uint32_t *>(row + k) = w[q];
-      } else {
-        unsigned short *p = reinterpret_cast<unsigned short *>(row + k);
-        if (k < K) p[0] = (unsigned short)(w[q]);
-        if (k + 1 < K) p[1] = (unsigned short)(w[q] >> 16);
+  for (int i = 0; i < 5; ++i) {
+    const size_t first = at - e + 8 * i;  // of the vector
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (first + 8 <= n) {
+      if (i < 4 || e) v = __ldg(p + i);
+    } else if (first < n) {  // the tensor's last, unfinished vector
+      uint32_t t[4] = {};
+      for (int q = 0; q < int(n - first); ++q) {
+        const uint32_t h = reinterpret_cast<const uint16_t *>(x)[first + q];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (u == q / 2) t[u] |= h << (16 * (q & 1));
       }
+      v = make_uint4(t[0], t[1], t[2], t[3]);
     }
+    a[4 * i] = v.x; a[4 * i + 1] = v.y; a[4 * i + 2] = v.z; a[4 * i + 3] = v.w;
   }
+#pragma unroll
+  for (int i = 0; i < 18; ++i) a[i] = (e & 4) ? a[i + 2] : a[i];
+#pragma unroll
+  for (int i = 0; i < 17; ++i) a[i] = (e & 2) ? a[i + 1] : a[i];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) w[i] = __byte_perm(a[i], a[i + 1], (e & 1) ? 0x5432u : 0x3210u);
 }
 
 // Four fp32 pairs as eight E2M1 codes, the first in the low nibble.
@@ -88,7 +85,7 @@ __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v) {
 
 // A block takes rows_per_block rows, a thread one 32-column group at a time of
 // their padded groups (4 per 128 columns, so that every scale byte is written).
-template <int ALIGN>
+template <bool ALIGNED>
 __global__ void __launch_bounds__(512)
     mx4_quantize_kernel(const __nv_bfloat16 *__restrict__ x, int rows, int K, size_t row_bytes,
                         int k_blocks, int rows_per_block, uint8_t *__restrict__ codes,
@@ -112,18 +109,27 @@ __global__ void __launch_bounds__(512)
       scale = 127;
       continue;
     }
-    const __nv_bfloat16 *xr = x + size_t(row) * K;
-    uint4 v[4];
+    uint32_t v[16];
+    const size_t at = size_t(row) * K + j * 32;
+    const int n = K - j * 32;
+    if constexpr (ALIGNED) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = load8<ALIGN>(xr, j * 32 + 8 * i, K);
+      for (int i = 0; i < 4; ++i) {
+        const uint4 r = 8 * i < n ? __ldg(reinterpret_cast<const uint4 *>(x + at) + i)
+                                  : make_uint4(0, 0, 0, 0);
+        v[4 * i] = r.x; v[4 * i + 1] = r.y; v[4 * i + 2] = r.z; v[4 * i + 3] = r.w;
+      }
+    } else {
+      load_group(x, at, size_t(rows) * K, v);
+      if (n < 32) {  // what follows is the next row's
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          v[i] = 2 * i + 1 < n ? v[i] : 2 * i < n ? v[i] & 0xFFFFu : 0u;
+      }
+    }
     __nv_bfloat162 m = as_bf16x2(0u);  // largest magnitudes; NaN stays
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      m = __hmax2_nan(m, __habs2(as_bf16x2(v[i].x)));
-      m = __hmax2_nan(m, __habs2(as_bf16x2(v[i].y)));
-      m = __hmax2_nan(m, __habs2(as_bf16x2(v[i].z)));
-      m = __hmax2_nan(m, __habs2(as_bf16x2(v[i].w)));
-    }
+    for (int i = 0; i < 16; ++i) m = __hmax2_nan(m, __habs2(as_bf16x2(v[i])));
     const uint32_t amax = max(as_u32(m) & 0x7FFFu, (as_u32(m) >> 16) & 0x7FFFu);
     const bool nan = amax > 0x7F80u;
     const int byte = max(int(amax >> 7) - 2, 0);  // X + 127
@@ -132,11 +138,11 @@ __global__ void __launch_bounds__(512)
     uint32_t c[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
       float f[8];
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        f2_unpack(f2_mul(f2_pack(bf16_lo(w[q]), bf16_hi(w[q])), inv2), f[2 * q], f[2 * q + 1]);
+        f2_unpack(f2_mul(f2_pack(bf16_lo(v[4 * i + q]), bf16_hi(v[4 * i + q])), inv2), f[2 * q],
+                  f[2 * q + 1]);
       c[i] = nan ? 0u : e2m1x8(f);
     }
     *reinterpret_cast<uint4 *>(codes + size_t(row) * row_bytes + j * 16) =
@@ -145,26 +151,34 @@ __global__ void __launch_bounds__(512)
   }
 }
 
-// Four E2M1 codes (16 bits) as two bf16 words, times s (a power of two, twice).
-// A magnitude's high and low byte are looked up by byte permutation (codes 0..7
-// have bf16 bits 0000 3F00 3F80 3FC0 4000 4040 4080 40C0).  A third permutation
-// takes the codes whole: a nibble's top bit makes it replicate the picked byte's
-// top bit, FF for a negative code and 80 for a positive one, which shifted by one
-// has the sign where the high byte wants it.
-__device__ __forceinline__ void e2m1_to_bf16(uint32_t code, __nv_bfloat162 s, uint32_t &w0,
+// Four E2M1 codes (16 bits) as two bf16 words, times s0 and s1 (powers of two for
+// the two values of a word each).  A magnitude's high and low byte are looked up
+// by byte permutation (codes 0..7 have bf16 bits 0000 3F00 3F80 3FC0 4000 4040 4080
+// 40C0).  A third permutation takes the codes whole: a nibble's top bit makes it
+// replicate the picked byte's top bit, FF for a negative code and 80 for a positive
+// one, which shifted by one has the sign where the high byte wants it.
+__device__ __forceinline__ void e2m1_to_bf16(uint32_t code, uint32_t s0, uint32_t s1, uint32_t &w0,
                                              uint32_t &w1) {
   const uint32_t c = code & 0x7777u;
   uint32_t sign;  // (the intrinsic ignores the selectors' top bits)
   asm("prmt.b32 %0, %1, %1, %2;" : "=r"(sign) : "r"(0x80808080u), "r"(code));
   const uint32_t lo = __byte_perm(0xC0800000u, 0xC0804000u, c);
   const uint32_t hi = __byte_perm(0x3F3F3F00u, 0x40404040u, c) | ((sign << 1) & 0x80808080u);
-  w0 = as_u32(__hmul2_rn(as_bf16x2(__byte_perm(lo, hi, 0x5140u)), s));
-  w1 = as_u32(__hmul2_rn(as_bf16x2(__byte_perm(lo, hi, 0x7362u)), s));
+  w0 = as_u32(__hmul2_rn(as_bf16x2(__byte_perm(lo, hi, 0x5140u)), as_bf16x2(s0)));
+  w1 = as_u32(__hmul2_rn(as_bf16x2(__byte_perm(lo, hi, 0x7362u)), as_bf16x2(s1)));
 }
 
-// blockDim.y rows a block; a row's blockDim.x threads take 8 columns at a time,
-// four loads in flight.
-template <int ALIGN>
+// 2^X in bf16, twice: the scale byte is its exponent field (2^-127 is subnormal,
+// 255 is NaN).
+__device__ __forceinline__ uint32_t scale_bf16x2(uint32_t byte) {
+  return (byte == 255u ? 0x7FC0u : byte == 0u ? 0x0040u : byte << 7) * 0x10001u;
+}
+
+// blockDim.y rows a block; a row's blockDim.x threads take its 16-byte vectors, four
+// loads in flight.  With the row's first column e elements into a vector, vector m
+// holds columns 8 m - e on: its codes are those of word m and the e nibbles before
+// it, which may belong to the group before.
+template <bool ALIGNED>
 __global__ void __launch_bounds__(512)
     mx4_dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
                           int rows, int K, size_t row_bytes, int k_blocks,
@@ -173,29 +187,55 @@ __global__ void __launch_bounds__(512)
   pdl_wait();
   const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
   if (row >= rows) return;
-  const int nvec = (K + 7) / 8, step = blockDim.x, rr = int(row & 127);
+  const size_t r0 = size_t(row) * K;
+  const int e = ALIGNED ? 0 : int(r0 & 7);
+  const int nvec = (K + e + 7) / 8, words = (K + 7) / 8, step = blockDim.x, rr = int(row & 127);
   const uint32_t *cr = reinterpret_cast<const uint32_t *>(codes + size_t(row) * row_bytes);
   const uint8_t *sr = scales + size_t(row >> 7) * k_blocks * 512 + (rr & 31) * 16 + (rr >> 5) * 4;
-  __nv_bfloat16 *yr = y + size_t(row) * K;
+  auto code_at = [&](int m) { return m >= 0 && m < words ? __ldg(cr + m) : 0u; };
+  auto scale_at = [&](int m) {
+    return m >= 0 && (m >> 2) * 32 < K ? uint32_t(__ldg(sr + size_t(m >> 4) * 512 + ((m >> 2) & 3)))
+                                       : 0u;
+  };
+  __nv_bfloat16 *yr = y + r0 - e;
   for (int j0 = threadIdx.x; j0 < nvec; j0 += kBatch * step) {
-    uint32_t c[kBatch], sc[kBatch];
+    uint32_t c[kBatch], sc[kBatch], sp[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const int j = j0 + i * step;
-      c[i] = j < nvec ? __ldg(cr + j) : 0u;
-      sc[i] = j < nvec ? __ldg(sr + size_t(j >> 4) * 512 + ((j >> 2) & 3)) : 0u;
+      const int m = j0 + i * step;
+      c[i] = code_at(m);
+      sp[i] = sc[i] = scale_at(m);
+      if constexpr (!ALIGNED) {
+        if (e) {
+          c[i] = __funnelshift_rc(code_at(m - 1), c[i], 4 * (8 - e));
+          if ((m & 3) == 0) sp[i] = scale_at(m - 1);
+        }
+      }
     }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const int j = j0 + i * step;
-      if (j >= nvec) break;
-      // 2^X in bf16: the byte is its exponent field (2^-127 is subnormal)
-      const uint32_t b = sc[i] == 255u ? 0x7FC0u : sc[i] == 0u ? 0x0040u : sc[i] << 7;
-      const __nv_bfloat162 s = as_bf16x2(b * 0x10001u);
+      const int m = j0 + i * step;
+      if (m >= nvec) break;
+      const uint32_t cur = scale_bf16x2(sc[i]);
+      uint32_t s[4] = {cur, cur, cur, cur};
+      if constexpr (!ALIGNED) {
+        const uint32_t prev = scale_bf16x2(sp[i]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)  // the first e values are the group's before
+          s[q] = 2 * q + 1 < e ? prev : 2 * q < e ? (prev & 0xFFFFu) | (cur & 0xFFFF0000u) : cur;
+      }
       uint32_t w[4];
-      e2m1_to_bf16(c[i], s, w[0], w[1]);
-      e2m1_to_bf16(c[i] >> 16, s, w[2], w[3]);
-      store8<ALIGN>(yr, j * 8, K, w);
+      e2m1_to_bf16(c[i], s[0], s[1], w[0], w[1]);
+      e2m1_to_bf16(c[i] >> 16, s[2], s[3], w[2], w[3]);
+      const int k0 = 8 * m - e;
+      if (ALIGNED || (k0 >= 0 && k0 + 8 <= K)) {
+        *reinterpret_cast<uint4 *>(yr + 8 * m) = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {  // a vector that the row shares with its neighbours
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (k0 + q >= 0 && k0 + q < K)
+            reinterpret_cast<uint16_t *>(yr)[8 * m + q] = uint16_t(w[q / 2] >> (16 * (q & 1)));
+      }
     }
   }
 }
@@ -218,8 +258,7 @@ cudaError_t launch_mx4_quantize(const void *x, int rows, int K, uint8_t *codes, 
   const int k_blocks = (K + 127) / 128;
   const Split sp(4 * k_blocks, 512);
   const long long grid = (((long long)rows + 127) / 128 * 128 + sp.rows - 1) / sp.rows;
-  auto kern = K % 8 == 0 ? mx4_quantize_kernel<8>
-                         : K % 2 == 0 ? mx4_quantize_kernel<2> : mx4_quantize_kernel<1>;
+  auto kern = K % 8 == 0 ? mx4_quantize_kernel<true> : mx4_quantize_kernel<false>;
   return launch_pdl(kern, dim3(unsigned(grid)), dim3(sp.threads), 0, st, 1,
                     static_cast<const __nv_bfloat16 *>(x), rows, K, mx4_row_bytes(K), k_blocks,
                     sp.rows, codes, scales);
@@ -231,8 +270,7 @@ cudaError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, i
   const int nvec = (K + 7) / 8, per = nvec >= 32 * kBatch ? kBatch : 2;
   const int tx = std::min(512, (nvec + per - 1) / per), ty = std::max(1, 256 / tx);
   const long long grid = ((long long)rows + ty - 1) / ty;
-  auto kern = K % 8 == 0 ? mx4_dequantize_kernel<8>
-                         : K % 2 == 0 ? mx4_dequantize_kernel<2> : mx4_dequantize_kernel<1>;
+  auto kern = K % 8 == 0 ? mx4_dequantize_kernel<true> : mx4_dequantize_kernel<false>;
   return launch_pdl(kern, dim3(unsigned(grid)), dim3(tx, ty), 0, st, 1, codes, scales, rows, K,
                     mx4_row_bytes(K), (K + 127) / 128, static_cast<__nv_bfloat16 *>(y));
 }
