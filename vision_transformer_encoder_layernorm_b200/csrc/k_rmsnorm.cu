@@ -72,6 +72,13 @@ struct RowVec<float> {
   }
 };
 
+__device__ __forceinline__ __nv_bfloat162 as_bf16x2(uint32_t v) {
+  return *reinterpret_cast<const __nv_bfloat162 *>(&v);
+}
+__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v) {
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+
 // An fp32 value that rounds to the same bf16 as v does: v rounded to fp32,
 // moved off a bf16 midpoint to the side v lies on.
 __device__ __forceinline__ float bf16_side(double v) {
@@ -245,7 +252,7 @@ __global__ void __launch_bounds__(V == 5 ? 512 : 1024, V == 5 ? 2 : 1)
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = t + tpr * i;
-    if (MX8 ? (c & ~15) * N >= k_blocks * 128 : c >= nvec) break;
+    if (MX8 ? (c & ~31) >= 16 * k_blocks : c >= nvec) break;  // MX8: whole warps
     const bool ok = active && c < nvec;
     const uint4 gv = ok ? __ldg(gr + c) : make_uint4(0, 0, 0, 0);
     float a[N], g[N], o[N];
@@ -287,35 +294,40 @@ __global__ void __launch_bounds__(V == 5 ? 512 : 1024, V == 5 ? 2 : 1)
     if constexpr (!MX8) {
       yr[c] = packed;
     } else {
+      if (!ok) packed = make_uint4(0, 0, 0, 0);
       float q[N];
-      R::unpack(ok ? packed : make_uint4(0, 0, 0, 0), q);
-      float amax = 0.f;
-#pragma unroll
-      for (int e = 0; e < N; ++e) amax = fmaxf(amax, fabsf(q[e]));
-      // sixteen lanes hold 128 columns and none of them has left the loop
-      const uint32_t mask = 0xFFFFu << (lane & 16);
-      amax = fmaxf(amax, __shfl_xor_sync(mask, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(mask, amax, 2));
-      const int ef = int(__float_as_uint(amax) >> 23) & 0xFF;
+      R::unpack(packed, q);
+      __nv_bfloat162 m = __hmax2(__habs2(as_bf16x2(packed.x)), __habs2(as_bf16x2(packed.y)));
+      m = __hmax2(m, __habs2(as_bf16x2(packed.z)));
+      m = __hmax2(m, __habs2(as_bf16x2(packed.w)));
+      m = __hmax2(m, as_bf16x2(0u));  // NaN drops out, as in the quantiser
+      const uint32_t mw = as_u32(m);
+      uint32_t amax = max(mw & 0xFFFFu, mw >> 16);  // bf16 magnitudes order as integers
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      const int ef = int(amax >> 7);
       const int X = ef == 0 ? -127 : max(ef - 127 - 8, -127);
       const float inv = __uint_as_float(uint32_t(127 - X) << 23);
       if (ok) {
         uint32_t w[2];
 #pragma unroll
+        for (int e = 0; e < N; e += 2)
+          f2_unpack(f2_mul(f2_pack(q[e], q[e + 1]), f2_pack(inv, inv)), q[e], q[e + 1]);
+#pragma unroll
         for (int p = 0; p < 2; ++p) {
           const uint32_t lo = __nv_cvt_float2_to_fp8x2(
-              make_float2(q[4 * p] * inv, q[4 * p + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+              make_float2(q[4 * p], q[4 * p + 1]), __NV_SATFINITE, __NV_E4M3);
           const uint32_t hi = __nv_cvt_float2_to_fp8x2(
-              make_float2(q[4 * p + 2] * inv, q[4 * p + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+              make_float2(q[4 * p + 2], q[4 * p + 3]), __NV_SATFINITE, __NV_E4M3);
           w[p] = (lo & 0xFFFFu) | ((hi & 0xFFFFu) << 16);
         }
         reinterpret_cast<uint2 *>(codes + size_t(row) * row_bytes)[c] = make_uint2(w[0], w[1]);
       }
       const bool group = active && (c & ~3) < nvec;  // the group has a column
       uint32_t word = uint32_t(group ? X + 127 : 127) << (8 * ((lane >> 2) & 3));
-      word |= __shfl_xor_sync(mask, word, 4);
-      word |= __shfl_xor_sync(mask, word, 8);
-      if ((lane & 15) == 0) {
+      word |= __shfl_xor_sync(0xffffffffu, word, 4);
+      word |= __shfl_xor_sync(0xffffffffu, word, 8);
+      if ((lane & 15) == 0 && c < 16 * k_blocks) {
         const int r = int(row & 127);
         uint8_t *block = scales + (size_t(row >> 7) * k_blocks + (c >> 4)) * 512;
         *reinterpret_cast<uint32_t *>(block + (r & 31) * 16 + (r >> 5) * 4) = word;
