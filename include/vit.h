@@ -486,7 +486,8 @@ VIT_API size_t vit_mx4_scale_bytes(int rows, int K);
  * is written.  Per 32-element group: X = floor(log2 max|x|) - 2 clamped to
  * [-127, 127] (-127 for an all-zero group), code = E2M1(x / 2^X) rounded to
  * nearest even, magnitudes above 6 (infinities too) clamped to 6; a group with
- * a NaN has scale byte 255 and zero codes.  Errors as vit_mx8_quantize. */
+ * a NaN has scale byte 255 and zero codes.  The buffers do not overlap; sizes up
+ * to 2^30.  Errors as vit_mx8_quantize. */
 VIT_API vit_status vit_mx4_quantize(vit_ctx *ctx, const void *x, int rows, int K, void *codes,
                                     void *scales, void *stream);
 
@@ -500,7 +501,9 @@ VIT_API vit_status vit_mx4_dequantize(vit_ctx *ctx, const void *codes, const voi
  * [M, K] and W = (w_codes, w_scales) [N, K], both MXFP4 along K (any K >= 1);
  * bias bf16 [N] or NULL; residual bf16 [M, N] for VIT_EPI_BIAS_RESIDUAL (may
  * be y: in place).  fp32 accumulation on the tensor core (block-scaled MMA).
- * N a multiple of 8.  Errors as vit_linear_mx8. */
+ * N a multiple of 8; sizes up to 2^30.  The order of summation goes by the sizes
+ * alone, so equal calls give equal bits.  y overlaps nothing but the residual it
+ * may replace.  Errors as vit_linear_mx8. */
 VIT_API vit_status vit_linear_mx4(vit_ctx *ctx, const void *a_codes, const void *a_scales,
                                   const void *w_codes, const void *w_scales, const void *bias,
                                   const void *residual, void *y, int M, int N, int K,

@@ -150,7 +150,9 @@ def test_mx4_refusals():
                {"b": P[4] + 8}, {"y": P[0]}, {"y": P[3] + 16}, {"y": P[4]},
                {"epi": 2, "res": P[5] + 16}):
         assert lin(**kw) == BAD, kw
+    big = (1 << 30) + 8
     assert lin(f) == UNSUP and lin(N=12) == UNSUP and lin(M=0) == 0
+    assert lin(M=big) == UNSUP and lin(N=big) == UNSUP and lin(K=big) == UNSUP
 
 
 def test_rope3d_refusals():

@@ -26,9 +26,9 @@
 // tensor memory), completing on the leader's barriers; the leader issues.
 //
 // Two accumulators of 256 columns and the 24 scale columns do not fit in the
-// 512 TMEM columns, so the 256-wide accumulators share 24 columns: a tile's
-// epilogue drains the shared end first, and only then may the next tile's MMAs
-// start, which by then is all but the whole accumulator early.
+// 512 TMEM columns, so the 256-wide accumulators share 24 columns: the next tile's
+// MMAs start once the epilogue's warps have read their 64 columns each into
+// registers, before they finish and store them.
 #include <cuda_bf16.h>
 #include <stdio.h>
 #include <stdlib.h>

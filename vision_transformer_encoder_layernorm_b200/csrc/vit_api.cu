@@ -1133,13 +1133,14 @@ size_t vit_mx4_scale_bytes(int rows, int K) {
 
 namespace {
 
-// Column counts up to here keep the kernels' 32-bit column arithmetic.
-constexpr int kMaxMx4Cols = 1 << 30;
+// Rows and columns up to here keep the kernels' 32-bit coordinates.
+constexpr int kMaxMx4Size = 1 << 30;
 
 vit_status check_mx4_matrix(const vit_ctx *ctx, const void *x, const void *codes,
                             const void *scales, int rows, int K) {
   if (!ctx || !x || !codes || !scales || rows < 0 || K < 0) return VIT_ERR_INVALID_ARG;
-  if (ctx->cfg.dtype != VIT_BF16 || K > kMaxMx4Cols) return VIT_ERR_UNSUPPORTED;
+  if (ctx->cfg.dtype != VIT_BF16 || rows > kMaxMx4Size || K > kMaxMx4Size)
+    return VIT_ERR_UNSUPPORTED;
   if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return VIT_ERR_INVALID_ARG;
   const size_t n = size_t(rows) * K * 2, nc = size_t(rows) * mx4_row_bytes(K),
                ns = mx4_scale_bytes(rows, K);
@@ -1183,7 +1184,9 @@ vit_status vit_linear_mx4(vit_ctx *ctx, const void *a_codes, const void *a_scale
   if (epi != VIT_EPI_BIAS && epi != VIT_EPI_BIAS_GELU && epi != VIT_EPI_BIAS_RESIDUAL)
     return VIT_ERR_INVALID_ARG;
   if (epi == VIT_EPI_BIAS_RESIDUAL && !residual) return VIT_ERR_INVALID_ARG;
-  if (ctx->cfg.dtype != VIT_BF16 || N % 8 || K > kMaxMx4Cols) return VIT_ERR_UNSUPPORTED;
+  if (ctx->cfg.dtype != VIT_BF16 || N % 8 || M > kMaxMx4Size || N > kMaxMx4Size ||
+      K > kMaxMx4Size)
+    return VIT_ERR_UNSUPPORTED;
   const void *ps[7] = {a_codes, a_scales, w_codes, w_scales, bias, residual, y};
   for (const void *p : ps)
     if (p && !aligned16(p)) return VIT_ERR_INVALID_ARG;
