@@ -165,9 +165,8 @@ __device__ __forceinline__ double inverse_root(double v) {
 
 // A row takes blockDim.x threads (whole warps), thread t holding the 16-byte
 // vectors t, t + blockDim.x, ... (V at most); blockDim.y rows a block.  MX8: y
-// goes out as codes and scales; four neighbouring threads hold a 32-column group,
-// sixteen the 128 columns whose four scale bytes make one word of the scale
-// blocks.  The MX8 grid covers the padded rows of the last block row, whose scale
+// goes out as codes and scales; four neighbouring threads hold a 32-column group.
+// The MX8 grid covers the padded rows of the last block row, whose scale
 // bytes are 127.  x, res, h and y may be the same buffers row by row: a thread
 // reads its vectors before it writes them, and no other thread touches them.
 template <typename T, bool MX8, int V>
@@ -249,6 +248,8 @@ __global__ void __launch_bounds__(V == 5 ? 512 : 1024, V == 5 ? 2 : 1)
   }
   const uint4 *gr = reinterpret_cast<const uint4 *>(gamma);
   uint4 *yr = reinterpret_cast<uint4 *>(y) + base;
+  uint8_t *crow = codes + (active ? size_t(row) * row_bytes : 0);
+  uint8_t *srow = scales + size_t(row >> 7) * k_blocks * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = t + tpr * i;
@@ -321,17 +322,10 @@ __global__ void __launch_bounds__(V == 5 ? 512 : 1024, V == 5 ? 2 : 1)
               make_float2(q[4 * p + 2], q[4 * p + 3]), __NV_SATFINITE, __NV_E4M3);
           w[p] = (lo & 0xFFFFu) | ((hi & 0xFFFFu) << 16);
         }
-        reinterpret_cast<uint2 *>(codes + size_t(row) * row_bytes)[c] = make_uint2(w[0], w[1]);
+        reinterpret_cast<uint2 *>(crow)[c] = make_uint2(w[0], w[1]);
       }
-      const bool group = active && (c & ~3) < nvec;  // the group has a column
-      uint32_t word = uint32_t(group ? X + 127 : 127) << (8 * ((lane >> 2) & 3));
-      word |= __shfl_xor_sync(0xffffffffu, word, 4);
-      word |= __shfl_xor_sync(0xffffffffu, word, 8);
-      if ((lane & 15) == 0 && c < 16 * k_blocks) {
-        const int r = int(row & 127);
-        uint8_t *block = scales + (size_t(row >> 7) * k_blocks + (c >> 4)) * 512;
-        *reinterpret_cast<uint32_t *>(block + (r & 31) * 16 + (r >> 5) * 4) = word;
-      }
+      if ((lane & 3) == 0 && c < 16 * k_blocks)
+        srow[size_t(c >> 4) * 512 + ((c >> 2) & 3)] = ok ? uint8_t(X + 127) : uint8_t(127);
     }
   }
 }
