@@ -286,19 +286,20 @@ class Context:
             raise VitError(fn, 2)
 
     def __getattr__(self, name):
-        # the types to compare with, once torch is needed
-        if name in ("_element", "_u8"):
+        # what these calls need of torch, from the first of them on
+        if name in ("_element", "_u8", "_i32", "_current", "_eps", "_head_dim"):
             import torch
+            self._eps, self._head_dim = self.cfg.ln_eps, self.cfg.head_dim
             self._element = torch.bfloat16 if self.cfg.dtype == BF16 else torch.float32
-            self._u8 = torch.uint8
+            self._u8, self._i32 = torch.uint8, torch.int32
+            self._current = torch._C._cuda_getCurrentRawStream
             return self.__dict__[name]
         raise AttributeError(name)
 
     def _on(self, stream):
         """The given stream, or the current one of the context's device."""
         if stream is None:
-            import torch
-            return torch._C._cuda_getCurrentRawStream(self._device)
+            return self._current(self._device)
         return stream if isinstance(stream, int) else stream.cuda_stream
 
     @property
@@ -454,7 +455,7 @@ class Context:
         _check("vit_rmsnorm", lib.vit_rmsnorm(
             self._h, x.data_ptr(), None if residual is None else residual.data_ptr(),
             gamma.data_ptr(), None if h is None else h.data_ptr(), y.data_ptr(), rows, cols,
-            self.cfg.ln_eps if eps is None else eps, self._on(stream)))
+            self._eps if eps is None else eps, self._on(stream)))
 
     def rmsnorm_mx8(self, x, gamma, codes, scales, residual=None, h=None, eps=None, stream=None):
         """vit_rmsnorm_mx8: rmsnorm straight to MXFP8 codes / scales (the layout
@@ -468,7 +469,7 @@ class Context:
         _check("vit_rmsnorm_mx8", lib.vit_rmsnorm_mx8(
             self._h, x.data_ptr(), None if residual is None else residual.data_ptr(),
             gamma.data_ptr(), None if h is None else h.data_ptr(), rows, cols,
-            self.cfg.ln_eps if eps is None else eps, codes.data_ptr(), scales.data_ptr(),
+            self._eps if eps is None else eps, codes.data_ptr(), scales.data_ptr(),
             self._on(stream)))
 
     def mx4_quantize(self, x, codes, scales, stream=None):
@@ -516,7 +517,6 @@ class Context:
     def rope3d(self, x, pos_thw, sections, layout=ROPE_BLOCKS, out=None, stream=None):
         """vit_rope3d on x [T, heads, head_dim] (rows of a wider tensor may be
         sliced: only the token stride is free), into ``out`` or in place."""
-        import torch
         fn = "vit_rope3d"
         shape = x.shape
         T, heads, d = shape
@@ -527,13 +527,13 @@ class Context:
             if t.dtype is not dt or t.get_device() != dev:
                 raise VitError(fn, 1)
             st = t.stride()
-            if t.shape != shape or d != self.cfg.head_dim or len(sections) != 3:
+            if t.shape != shape or d != self._head_dim or len(sections) != 3:
                 raise VitError(fn, 2)
             if T and heads and ((heads > 1 and st[1] != d) or st[2] != 1):
                 raise VitError(fn, 1)
             # a single token has no stride to go by
             strides.append(max(st[0], heads * d) if T <= 1 else st[0])
-        if (pos_thw.dtype is not torch.int32 or pos_thw.get_device() != dev
+        if (pos_thw.dtype is not self._i32 or pos_thw.get_device() != dev
                 or not pos_thw.is_contiguous()):
             raise VitError(fn, 1)
         if pos_thw.shape != (T, 3):
