@@ -19,7 +19,8 @@ __all__ = [
     "lib", "LIB_PATH", "VitError", "VitConfig", "VitLayerWeights", "VitProjectorWeights",
     "VitSeqs", "Context",
     "F32", "BF16", "FLAG_NO_ROPE", "FLAG_NO_MLP", "EPI_BIAS", "EPI_BIAS_GELU",
-    "EPI_BIAS_RESIDUAL", "ROPE_BLOCKS", "ROPE_SECTIONS", "ROPE_TURNS", "STATUS", "ABI_FUNCTIONS", "KERNEL_KINDS", "Graph",
+    "EPI_BIAS_RESIDUAL", "ROPE_BLOCKS", "ROPE_SECTIONS", "ROPE_TURNS", "STATUS",
+    "ABI_FUNCTIONS", "KERNEL_KINDS", "Graph",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libvit.so")

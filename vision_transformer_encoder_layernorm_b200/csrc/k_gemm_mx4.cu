@@ -167,7 +167,8 @@ struct Prefetch {
 template <int BN, int EPI, bool PAIR>
 __global__ void __launch_bounds__((Cfg<BN, PAIR>::kThreads), 1)
     gemm_mx4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                    const __grid_constant__ CUtensorMap tmSa, const __grid_constant__ CUtensorMap tmSb,
+                    const __grid_constant__ CUtensorMap tmSa,
+                    const __grid_constant__ CUtensorMap tmSb,
                     const __grid_constant__ CUtensorMap tmR, const __grid_constant__ CUtensorMap tmY,
                     const __nv_bfloat16 *__restrict__ bias, int M, int N, int K, int *status,
                     const __grid_constant__ Prefetch pre) {
@@ -711,15 +712,17 @@ cudaError_t run_epi(const Args &g, int epi) {
 // The tile's shape by a cost model, in microseconds as measured over 3900 x
 // {1152, 3456, 4304} x {1152, 4304}, 960 x 4304 x 1152, 10936 x 1152 x 4304 and
 // 8192 x 4096 x 8192: a round over the SMs takes a tile's k-blocks or its
-// epilogue, whichever is longer (accumulators that share columns add a wait);
-// the first round's k-blocks and the last one's epilogue are not overlapped, a
-// pair starts later, and joining a split tile takes time by its rows and parts.  One CTA wins with few k-blocks and tiles (960 x 4304
-// x 1152: 6.8 us, pairs 7.6 to 8.5; 3900 x 1152 x 1152: 9.0 against 9.3), 192
-// columns for the wide projections (3900 x 4304 x 1152: 15.4, 128 columns 17.5,
-// 256 16.0, one CTA 18.3), 256 for the most work per byte (10936 x 1152 x 4304:
-// 35.4 against 42.0 at 128; 8192 x 4096 x 8192: 99 against 122), split tiles for few
-// rows over a long K (1 x 1152 x 4304: 7.8, over 8 CTAs 4.1; 64 rows: 9.0, over 4
-// CTAs 7.3, over 8 8.6; 1 x 3456 x 1152: 3.7 either way).
+// epilogue, whichever is longer (accumulators that share columns add a wait); the
+// first round's k-blocks and the last one's epilogue are not overlapped, a pair
+// starts later, and joining a split tile takes time by its rows and parts.
+//  - One CTA wins with few k-blocks and tiles (960 x 4304 x 1152: 6.8 us, pairs
+//    7.6 to 8.5; 3900 x 1152 x 1152: 9.0 against 9.3);
+//  - 192 columns for the wide projections (3900 x 4304 x 1152: 15.4, 128 columns
+//    17.5, 256 16.0, one CTA 18.3);
+//  - 256 for the most work per byte (10936 x 1152 x 4304: 35.4 against 42.0 at 128;
+//    8192 x 4096 x 8192: 99 against 122);
+//  - split tiles for few rows over a long K (1 x 1152 x 4304: 7.8, over 8 CTAs 4.1;
+//    64 rows: 9.0, over 4 CTAs 7.3, over 8 8.6; 1 x 3456 x 1152: 3.7 either way).
 struct Shape {
   int ctas, bn, split;
   float kblock, epilogue, wait, start;

@@ -11,7 +11,9 @@
 // the dequantiser), with instructions close behind: at 6.4 TB/s an SM has about
 // 16 issue slots an element.  The quantiser gives a thread a whole group, so the
 // scale is found once for 32 elements; the dequantiser gives it 8 columns (a word
-// of codes, 16 bytes out), so that its stores are whole lines.
+// of codes, 16 bytes out), so that its stores are whole lines.  10936 x 4304: 20.2
+// us (5910 GB/s, 92% of the measured copy rate) and 23.3 us (5120 GB/s, 72% of the
+// issue slots).
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -25,9 +27,9 @@ namespace {
 constexpr int kBatch = 4;  // vectors of 8 columns a dequantising thread has in flight
 
 // Rows of K % 8 != 0 columns start anywhere in a 16-byte vector.  Memory is still
-// read and written in whole aligned vectors, and shifted in registers: accesses of
-// one bf16 at a time took 26 us for both ways over 3900 x 1151, against 11 for
-// 3900 x 1152.
+// read and written in whole aligned vectors, and shifted in registers: 3900 x 1151
+// takes 4.6 and 7.1 us (3900 x 1152: 4.2 and 3.8), by accesses of one bf16 at a time
+// 10.1 and 20.3.
 
 // 32 elements from element `at` of x (n elements in all, 16-byte aligned), the ones
 // past n zero.

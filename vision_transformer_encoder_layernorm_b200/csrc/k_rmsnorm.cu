@@ -5,7 +5,10 @@
 //
 // Bound: HBM.  x and residual are read once, h and y written once (8 bytes a
 // bf16 element, 7 with MXFP8 codes); the row stays in registers between the
-// sum of squares and the output.
+// sum of squares and the output.  10936 x 1152 with residual takes 19.9 us (5070
+// GB/s, 79% of the measured copy rate), 3900 x 1152 to MXFP8 10.4 us: there all rows
+// are resident at once, and a warp's 1200 instructions after its loads are what is
+// left.
 //
 // Numerics.  The squares are summed in fp64, so neither large rows overflow nor
 // long ones lose bits, and a bf16 output is the correctly rounded value of the
@@ -348,7 +351,7 @@ cudaError_t run(const void *x, const void *res, const void *gamma, void *h, void
 // allows): each thread's code is short (1 row of 1152 columns 1.9 us, with five
 // 3.0).  Where the rows need more threads than the SMs hold at once, five: the
 // row's reduction and its root are then shared by more columns (10936 x 1152: 19.9
-// us, with one 31.0).
+// us, with one 27.9, with three 20.6).
 template <typename T, bool MX8>
 cudaError_t pick(const void *x, const void *res, const void *gamma, void *h, void *y, int rows,
                  int cols, float eps, uint8_t *codes, uint8_t *scales, int num_sms,

@@ -15,7 +15,9 @@
 // pairs (up to 16 bytes of each half) of one token and keeps their cos and sin
 // in registers over the token's heads, four heads' loads in flight at a time;
 // the block's cos/sin table (tokens x d/2) is computed while the first four
-// are on their way.
+// are on their way.  16384 tokens x 32 heads of 128: 43.4 us (6200 GB/s, 96% of the
+// measured copy rate); kept as fp32 in flight, the heads took 128 registers, left two
+// blocks an SM and took 81 us.
 #include "kernels.h"
 
 namespace vit {
