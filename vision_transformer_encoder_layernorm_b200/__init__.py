@@ -7,6 +7,8 @@ merge.
 This module only marshals arguments: every step runs in the CUDA kernels of
 ``libvit.so``.  There is no fallback; importing fails loudly when the library
 has not been built (``python vision_transformer_encoder_layernorm_b200/build.py``).
+Most calls go through ctypes; RMSNorm, MXFP4 and three-axis RoPE, which also check
+their tensors, through the extension module ``_marshal`` (csrc/marshal.c).
 Tensors are PyTorch tensors (device memory and streams only).
 """
 from __future__ import annotations
@@ -79,7 +81,6 @@ class VitSeqs(ctypes.Structure):
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
-_Int3 = ctypes.c_int32 * 3
 # name -> (restype, argtypes); the exported C ABI of include/vit.h
 ABI_FUNCTIONS = {
     "vit_init": (_I, [ctypes.POINTER(VitConfig), _I, ctypes.POINTER(_P)]),
@@ -154,7 +155,21 @@ def _load():
     return h
 
 
+def _load_marshal():
+    path = os.path.join(os.path.dirname(LIB_PATH), "_marshal.so")
+    if not os.path.exists(path):
+        raise ImportError(
+            f"{path} is missing: build it with "
+            "`python vision_transformer_encoder_layernorm_b200/build.py`")
+    from . import _marshal as m
+    m.bind(*(ctypes.cast(getattr(lib, name), _P).value for name in (
+        "vit_rmsnorm", "vit_rmsnorm_mx8", "vit_mx4_quantize", "vit_mx4_dequantize",
+        "vit_linear_mx4", "vit_rope3d")))
+    return m
+
+
 lib = _load()
+_marshal = _load_marshal()
 
 
 def _ptr(t) -> Optional[int]:
@@ -260,48 +275,18 @@ class Context:
         self._h = h
         self._device = device
 
-    # Checks of the entry points below that take tensors of a fixed layout: the C
-    # call sees bare pointers, so a wrong type, device, shape or stride is refused
-    # here.  They run on every call, so they ask a tensor for as little as they can.
-    def _dense(self, fn: str, shape, *tensors):
-        """Contiguous tensors (or None) of the context's element type and this
-        shape on its device."""
-        dt, dev = self._element, self._device
-        for t in tensors:
-            if t is not None:
-                if t.dtype is not dt or t.get_device() != dev or not t.is_contiguous():
-                    raise VitError(fn, 1)
-                if t.shape != shape:
-                    raise VitError(fn, 2)
-
-    def _codes(self, fn: str, codes, scales, rows: int, row_bytes: int, K: int):
-        """Contiguous byte tensors of at least the sizes of a [rows, K] matrix in
-        a microscaled format."""
-        u8, dev = self._u8, self._device
-        if (codes.dtype is not u8 or scales.dtype is not u8 or codes.get_device() != dev
-                or scales.get_device() != dev or not codes.is_contiguous()
-                or not scales.is_contiguous()):
-            raise VitError(fn, 1)
-        if (codes.numel() < rows * row_bytes
-                or scales.numel() < (rows + 127) // 128 * ((K + 127) // 128) * 512):
-            raise VitError(fn, 2)
-
     def __getattr__(self, name):
-        # what these calls need of torch, from the first of them on
-        if name in ("_element", "_u8", "_i32", "_current", "_eps", "_head_dim"):
-            import torch
-            self._eps, self._head_dim = self.cfg.ln_eps, self.cfg.head_dim
-            self._element = torch.bfloat16 if self.cfg.dtype == BF16 else torch.float32
-            self._u8, self._i32 = torch.uint8, torch.int32
-            self._current = torch._C._cuda_getCurrentRawStream
-            return self.__dict__[name]
-        raise AttributeError(name)
-
-    def _on(self, stream):
-        """The given stream, or the current one of the context's device."""
-        if stream is None:
-            return self._current(self._device)
-        return stream if isinstance(stream, int) else stream.cuda_stream
+        # the checked calls (csrc/marshal.c), from the first of them on: the C entry
+        # points see bare pointers, so a tensor of a wrong type, device, shape or
+        # stride is refused there
+        if name != "_calls":
+            raise AttributeError(name)
+        import torch
+        self._calls = _marshal.Calls(
+            self._h.value if isinstance(self._h, _P) else self._h,
+            torch.bfloat16 if self.cfg.dtype == BF16 else torch.float32, torch.uint8, torch.int32,
+            torch._C._cuda_getCurrentRawStream, self._device, self.cfg.ln_eps, self.cfg.head_dim)
+        return self._calls
 
     @property
     def handle(self):
@@ -309,6 +294,7 @@ class Context:
 
     def close(self):
         if getattr(self, "_h", None):
+            self.__dict__.pop("_calls", None)  # it holds the handle
             lib.vit_destroy(self._h)
             self._h = None
 
@@ -448,102 +434,43 @@ class Context:
     def rmsnorm(self, x, gamma, y, residual=None, h=None, eps=None, stream=None):
         """vit_rmsnorm: y = h / sqrt(mean(h^2) + eps) * gamma of h = x +
         residual (h = x without one); h, if given, receives the sum."""
-        rows, cols = x.shape
-        self._dense("vit_rmsnorm", (rows, cols), x, y, residual, h)
-        self._dense("vit_rmsnorm", (cols,), gamma)
-        if not rows:
-            return  # an empty tensor has no address to pass
-        _check("vit_rmsnorm", lib.vit_rmsnorm(
-            self._h, x.data_ptr(), None if residual is None else residual.data_ptr(),
-            gamma.data_ptr(), None if h is None else h.data_ptr(), y.data_ptr(), rows, cols,
-            self._eps if eps is None else eps, self._on(stream)))
+        code = self._calls.rmsnorm(x, gamma, y, residual, h, eps, stream)
+        if code:
+            raise VitError("vit_rmsnorm", code)
 
     def rmsnorm_mx8(self, x, gamma, codes, scales, residual=None, h=None, eps=None, stream=None):
         """vit_rmsnorm_mx8: rmsnorm straight to MXFP8 codes / scales (the layout
         of mx8_quantize)."""
-        rows, cols = x.shape
-        self._dense("vit_rmsnorm_mx8", (rows, cols), x, residual, h)
-        self._dense("vit_rmsnorm_mx8", (cols,), gamma)
-        self._codes("vit_rmsnorm_mx8", codes, scales, rows, (cols + 15) // 16 * 16, cols)
-        if not rows:
-            return
-        _check("vit_rmsnorm_mx8", lib.vit_rmsnorm_mx8(
-            self._h, x.data_ptr(), None if residual is None else residual.data_ptr(),
-            gamma.data_ptr(), None if h is None else h.data_ptr(), rows, cols,
-            self._eps if eps is None else eps, codes.data_ptr(), scales.data_ptr(),
-            self._on(stream)))
+        code = self._calls.rmsnorm_mx8(x, gamma, codes, scales, residual, h, eps, stream)
+        if code:
+            raise VitError("vit_rmsnorm_mx8", code)
 
     def mx4_quantize(self, x, codes, scales, stream=None):
         """bf16 x [rows, K] -> MXFP4 codes [rows, mx4_row_bytes(K)] (uint8) and
         scales [mx4_scale_bytes(rows, K)] (uint8), see vit_mx4_quantize."""
-        rows, K = x.shape
-        self._dense("vit_mx4_quantize", (rows, K), x)
-        self._codes("vit_mx4_quantize", codes, scales, rows, (K + 31) // 32 * 16, K)
-        if not rows or not K:
-            return
-        _check("vit_mx4_quantize", lib.vit_mx4_quantize(
-            self._h, x.data_ptr(), rows, K, codes.data_ptr(), scales.data_ptr(),
-            self._on(stream)))
+        code = self._calls.mx4_quantize(x, codes, scales, stream)
+        if code:
+            raise VitError("vit_mx4_quantize", code)
 
     def mx4_dequantize(self, codes, scales, y, stream=None):
         """MXFP4 codes and scales of a [rows, K] matrix -> bf16 y [rows, K]."""
-        rows, K = y.shape
-        self._dense("vit_mx4_dequantize", (rows, K), y)
-        self._codes("vit_mx4_dequantize", codes, scales, rows, (K + 31) // 32 * 16, K)
-        if not rows or not K:
-            return
-        _check("vit_mx4_dequantize", lib.vit_mx4_dequantize(
-            self._h, codes.data_ptr(), scales.data_ptr(), rows, K, y.data_ptr(),
-            self._on(stream)))
+        code = self._calls.mx4_dequantize(y, codes, scales, stream)
+        if code:
+            raise VitError("vit_mx4_dequantize", code)
 
     def linear_mx4(self, a, w, bias, y, K, epi=EPI_BIAS, residual=None, stream=None):
         """y = epi(deq(A) deq(W)^T + bias) with a = (codes, scales) [M, K] and
         w = (codes, scales) [N, K] from mx4_quantize."""
-        fn = "vit_linear_mx4"
-        M, N = y.shape
-        (ac, asc), (wc, wsc) = a, w
-        row_bytes = (K + 31) // 32 * 16
-        self._dense(fn, (M, N), y, residual)
-        self._dense(fn, (N,), bias)
-        self._codes(fn, ac, asc, M, row_bytes, K)
-        self._codes(fn, wc, wsc, N, row_bytes, K)
-        if not M:
-            return
-        _check(fn, lib.vit_linear_mx4(
-            self._h, ac.data_ptr(), asc.data_ptr(), wc.data_ptr(), wsc.data_ptr(),
-            None if bias is None else bias.data_ptr(),
-            None if residual is None else residual.data_ptr(), y.data_ptr(), M, N, K, epi,
-            self._on(stream)))
+        code = self._calls.linear_mx4(a[0], a[1], w[0], w[1], bias, residual, y, K, epi, stream)
+        if code:
+            raise VitError("vit_linear_mx4", code)
 
     def rope3d(self, x, pos_thw, sections, layout=ROPE_BLOCKS, out=None, stream=None):
         """vit_rope3d on x [T, heads, head_dim] (rows of a wider tensor may be
         sliced: only the token stride is free), into ``out`` or in place."""
-        fn = "vit_rope3d"
-        shape = x.shape
-        T, heads, d = shape
-        y = x if out is None else out
-        dt, dev = self._element, self._device
-        strides = []
-        for t in (x,) if out is None else (x, out):
-            if t.dtype is not dt or t.get_device() != dev:
-                raise VitError(fn, 1)
-            st = t.stride()
-            if t.shape != shape or d != self._head_dim or len(sections) != 3:
-                raise VitError(fn, 2)
-            if T and heads and ((heads > 1 and st[1] != d) or st[2] != 1):
-                raise VitError(fn, 1)
-            # a single token has no stride to go by
-            strides.append(max(st[0], heads * d) if T <= 1 else st[0])
-        if (pos_thw.dtype is not self._i32 or pos_thw.get_device() != dev
-                or not pos_thw.is_contiguous()):
-            raise VitError(fn, 1)
-        if pos_thw.shape != (T, 3):
-            raise VitError(fn, 2)
-        if not T:
-            return
-        _check(fn, lib.vit_rope3d(self._h, x.data_ptr(), strides[0], y.data_ptr(), strides[-1],
-                                  pos_thw.data_ptr(), T, heads, _Int3(*sections), layout,
-                                  self._on(stream)))
+        code = self._calls.rope3d(x, pos_thw, sections, layout, out, stream)
+        if code:
+            raise VitError("vit_rope3d", code)
 
     def rope2d(self, qkv, pos_rc, stream=None):
         _check("vit_rope2d", lib.vit_rope2d(self._h, _ptr(qkv), _ptr(pos_rc), qkv.shape[0],

@@ -12,10 +12,12 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libvit.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")  # CPython extension: argument marshalling
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["vit_api.cu", "k_rows.cu", "k_simt.cu", "k_gemm_tc.cu", "k_attn_tc.cu", "k_embed.cu", "k_mx8.cu",
@@ -36,13 +38,26 @@ def nvcc() -> str:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(MARSHAL):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     deps += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     deps.append(os.path.abspath(__file__))
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def build_marshal(verbose: bool = False) -> str:
+    """The binding's extension module, for the running Python."""
+    out_tmp = MARSHAL + ".tmp"
+    cmd = [os.environ.get("CC") or "gcc", "-O2", "-shared", "-fPIC", "-Wall",
+           "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "marshal.c"),
+           "-o", out_tmp]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(out_tmp, MARSHAL)
+    return MARSHAL
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
@@ -62,6 +77,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         if verbose:
             print(" ".join(cmd), flush=True)
         procs.append(subprocess.Popen(cmd))
+    build_marshal(verbose)
     failed = [c for c, p in zip(cmds, procs) if p.wait() != 0]
     if failed:
         raise RuntimeError("nvcc failed: " + " ".join(failed[0]))
