@@ -231,3 +231,17 @@ def test_binding_takes_empty_batches(ctx):
     ctx.linear_mx4((u(0, 48), u(0)), (u(16, 48), u(512)), b(16), b(0, 16), 70, stream=0)
     ctx.rope3d(b(0, 4, 72), torch.zeros(0, 3, dtype=torch.int32), (12, 12, 12), stream=0)
     refused(SHAPE, ctx.rmsnorm, b(0, 64), b(32), b(0, 64))  # checked all the same
+
+
+def test_closed_context_and_wrong_kinds_of_arguments(ctx):
+    b = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    refused(BAD, ctx.rmsnorm, b(4, 64), b(64), b(4, 64))  # all is well but the handle
+    for bad in (None, 3, "x"):
+        with pytest.raises((AttributeError, TypeError)):
+            ctx.rmsnorm(bad, b(64), b(4, 64), stream=0)
+        with pytest.raises((AttributeError, TypeError)):
+            ctx.rmsnorm(b(4, 64), b(64), bad, stream=0)
+    with pytest.raises(TypeError):
+        ctx.rope3d(b(5, 3, 72), torch.zeros(5, 3, dtype=torch.int32), (12, 12, 12.5), stream=0)
+    refused(SHAPE, ctx.rmsnorm, b(64), b(64), b(64))      # one dimension
+    refused(BAD, ctx.linear_mx4, (None, None), (None, None), None, b(4, 16), -1)
