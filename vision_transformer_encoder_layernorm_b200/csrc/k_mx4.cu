@@ -28,7 +28,7 @@ constexpr int kBatch = 4;  // vectors of 8 columns a dequantising thread has in 
 
 // Rows of K % 8 != 0 columns start anywhere in a 16-byte vector.  Memory is still
 // read and written in whole aligned vectors, and shifted in registers: 3900 x 1151
-// takes 4.6 and 7.1 us (3900 x 1152: 4.2 and 3.8), by accesses of one bf16 at a time
+// takes 4.6 and 5.8 us (3900 x 1152: 4.2 and 3.7), by accesses of one bf16 at a time
 // 10.1 and 20.3.
 
 // 32 elements from element `at` of x (n elements in all, 16-byte aligned), the ones
@@ -194,24 +194,24 @@ __global__ void __launch_bounds__(512)
   const int nvec = (K + e + 7) / 8, words = (K + 7) / 8, step = blockDim.x, rr = int(row & 127);
   const uint32_t *cr = reinterpret_cast<const uint32_t *>(codes + size_t(row) * row_bytes);
   const uint8_t *sr = scales + size_t(row >> 7) * k_blocks * 512 + (rr & 31) * 16 + (rr >> 5) * 4;
-  auto code_at = [&](int m) { return m >= 0 && m < words ? __ldg(cr + m) : 0u; };
   auto scale_at = [&](int m) {
-    return m >= 0 && (m >> 2) * 32 < K ? uint32_t(__ldg(sr + size_t(m >> 4) * 512 + ((m >> 2) & 3)))
-                                       : 0u;
+    return uint32_t(__ldg(sr + size_t(m >> 4) * 512 + ((m >> 2) & 3)));
   };
+  // which values of a vector are the e of the word before
+  uint32_t before[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) before[q] = 2 * q + 1 < e ? ~0u : 2 * q < e ? 0xFFFFu : 0u;
   __nv_bfloat16 *yr = y + r0 - e;
   for (int j0 = threadIdx.x; j0 < nvec; j0 += kBatch * step) {
     uint32_t c[kBatch], sc[kBatch], sp[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int m = j0 + i * step;
-      c[i] = code_at(m);
-      sp[i] = sc[i] = scale_at(m);
-      if constexpr (!ALIGNED) {
-        if (e) {
-          c[i] = __funnelshift_rc(code_at(m - 1), c[i], 4 * (8 - e));
-          if ((m & 3) == 0) sp[i] = scale_at(m - 1);
-        }
+      c[i] = m < words ? __ldg(cr + m) : 0u;
+      sp[i] = sc[i] = m < nvec ? scale_at(min(m, words - 1)) : 0u;
+      if (!ALIGNED && e && m < nvec) {
+        c[i] = __funnelshift_rc(m > 0 ? __ldg(cr + m - 1) : 0u, c[i], 4 * (8 - e));
+        if ((m & 3) == 0 && m > 0) sp[i] = scale_at(m - 1);
       }
     }
 #pragma unroll
@@ -223,8 +223,7 @@ __global__ void __launch_bounds__(512)
       if constexpr (!ALIGNED) {
         const uint32_t prev = scale_bf16x2(sp[i]);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)  // the first e values are the group's before
-          s[q] = 2 * q + 1 < e ? prev : 2 * q < e ? (prev & 0xFFFFu) | (cur & 0xFFFF0000u) : cur;
+        for (int q = 0; q < 4; ++q) s[q] = (prev & before[q]) | (cur & ~before[q]);
       }
       uint32_t w[4];
       e2m1_to_bf16(c[i], s[0], s[1], w[0], w[1]);
@@ -270,7 +269,9 @@ cudaError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, i
                                   void *y, cudaStream_t st) {
   // four vectors a thread, or two where that leaves a row under a warp of threads
   const int nvec = (K + 7) / 8, per = nvec >= 32 * kBatch ? kBatch : 2;
-  const int tx = std::min(512, (nvec + per - 1) / per), ty = std::max(1, 256 / tx);
+  int tx = std::min(512, (nvec + per - 1) / per);
+  if (K % 8) tx = (tx + 31) / 32 * 32;  // a warp's threads share a row's shift
+  const int ty = std::max(1, 256 / tx);
   const long long grid = ((long long)rows + ty - 1) / ty;
   auto kern = K % 8 == 0 ? mx4_dequantize_kernel<true> : mx4_dequantize_kernel<false>;
   return launch_pdl(kern, dim3(unsigned(grid)), dim3(tx, ty), 0, st, 1, codes, scales, rows, K,
