@@ -245,3 +245,13 @@ def test_closed_context_and_wrong_kinds_of_arguments(ctx):
         ctx.rope3d(b(5, 3, 72), torch.zeros(5, 3, dtype=torch.int32), (12, 12, 12.5), stream=0)
     refused(SHAPE, ctx.rmsnorm, b(64), b(64), b(64))      # one dimension
     refused(BAD, ctx.linear_mx4, (None, None), (None, None), None, b(4, 16), -1)
+
+
+def test_choices_past_an_int_are_refused_not_cut_off(ctx):
+    b = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    u = lambda *s: torch.zeros(*s, dtype=torch.uint8)     # noqa: E731
+    for v in (1 << 32, -(1 << 32), (1 << 32) + 1):        # 0 and 1 in their low 32 bits
+        refused(BAD, ctx.linear_mx4, (u(0, 48), u(0)), (u(16, 48), u(512)), None, b(0, 16), 70,
+                epi=v)
+        refused(BAD, ctx.rope3d, b(0, 4, 72), torch.zeros(0, 3, dtype=torch.int32), (12, 12, 12),
+                layout=v)

@@ -124,6 +124,9 @@ static int fits_int(const long long *v, int n) {
   return VIT_OK;
 }
 
+/* A choice (an enum of the C ABI) that its int holds. */
+static int is_int(long v) { return v >= INT_MIN && v <= INT_MAX; }
+
 /* The given stream (an integer, or an object with cuda_stream), or the device's
  * current one. */
 static int get_stream(const Calls *c, PyObject *o, void **st) {
@@ -236,7 +239,7 @@ static PyObject *calls_linear_mx4(Calls *c, PyObject *const *a, Py_ssize_t n) {
   K = PyLong_AsLongLong(a[7]);
   epi = PyLong_AsLong(a[8]);
   if (PyErr_Occurred()) return NULL;
-  if (K < 0) return result(VIT_ERR_INVALID_ARG);
+  if (K < 0 || !is_int(epi)) return result(VIT_ERR_INVALID_ARG);
   const long long row_bytes = (K + 31) / 32 * 16;
   if ((s = get_sizes(a[6], s_shape, 0, 2, sh)) || (s = fits_int(sh, 2)) || (s = fits_int(&K, 1)) ||
       (s = check_dense(c, a[6], c->element, 2, sh, 0, &y)) ||
@@ -277,6 +280,7 @@ static PyObject *calls_rope3d(Calls *c, PyObject *const *a, Py_ssize_t n) {
   if (!arity(n, 6)) return NULL;
   layout = PyLong_AsLong(a[3]);
   if (PyErr_Occurred()) return NULL;
+  if (!is_int(layout)) return result(VIT_ERR_INVALID_ARG);
   PyObject *seq = PySequence_Tuple(a[2]);
   if (!seq) return NULL;
   s = PyTuple_GET_SIZE(seq) == 3 ? VIT_OK : VIT_ERR_SHAPE;
