@@ -115,7 +115,7 @@ __device__ __forceinline__ float bf16_side2(float p, float rh, float rl) {
   const float s = hi + err, rest = err - (s - hi);
   uint32_t u = __float_as_uint(s);
   if ((u & 0xFFFFu) == 0x8000u && rest != 0.f) u += (rest > 0.f) == (s > 0.f) ? 1u : ~0u;
-  return __uint_as_float(u);
+  return __uint_as_float(u | (__float_as_uint(p) & 0x80000000u));  // -0 + 0 is 0
 }
 
 // Sum of squares of 16 bytes of a row.
