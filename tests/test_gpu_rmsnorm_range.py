@@ -1,4 +1,4 @@
-"""RMSNorm at the edges of its arithmetic.
+"""RMSNorm where h * gamma leaves the fp32 range although the result does not.
 
 bf16: y is the formula's value for the stored h rounded once to nearest.  The fp64
 reference is within 2^-50 of the formula, and a random value is closer than that to
@@ -67,3 +67,32 @@ def test_zeros_keep_their_sign(ctx):
     assert torch.all(torch.signbit(y[:, 1::2]))
     ctx.rmsnorm(-x, w, y, eps=1e-6)  # -0 times a negative gamma
     assert not torch.any(torch.signbit(y[:, 1::2]))
+
+
+@pytest.mark.parametrize("cols", [64, 1152, 4616])
+@pytest.mark.parametrize("row,gam,eps", [
+    (80, 60, 1e-6),     # the product overflows, the result is 2^60
+    (100, 27, 1e-6), (126, 100, 0.0),
+    (-90, -70, 0.0),    # the product underflows, the result is 2^-70
+    (-95, -48, 0.0),    # the product is subnormal and has lost bits
+    (-60, -70, 0.0), (-99, 126, 0.0), (-130, 20, 0.0), (0, -126, 1e-6), (0, 120, 1e-6),
+    (-20, -120, 0.0), (3, -130, 1e-6)])
+def test_products_out_of_range(ctx, cols, row, gam, eps):
+    g = np.random.Generator(np.random.PCG64(abs(row) + abs(gam)))
+    h = g.standard_normal((9, cols)) * 2.0 ** row
+    h[:, ::7] = 0
+    gamma = (1 + 0.3 * g.standard_normal(cols)) * 2.0 ** gam
+    check(ctx, np.clip(h, -3e38, 3e38), gamma, eps)
+    gamma[::3] = 1 + 0.3 * g.standard_normal(len(gamma[::3]))  # neighbours of ordinary size
+    check(ctx, np.clip(h, -3e38, 3e38), gamma, eps)
+
+
+@pytest.mark.parametrize("cols", [256, 1160])
+def test_values_of_every_size(ctx, cols):
+    """Rows of any size, elements far below their row's, gammas of any size."""
+    g = np.random.Generator(np.random.PCG64(cols))
+    rows = 200
+    h = g.standard_normal((rows, cols)) * np.exp2(g.integers(-126, 120, (rows, 1)) - g.integers(0, 60, (rows, cols)) * (g.random((rows, cols)) < 0.8))
+    gamma = g.standard_normal(cols) * np.exp2(g.integers(-126, 126, cols).astype(float))
+    check(ctx, h, gamma, 0.0)
+    check(ctx, h, gamma, 1e-6)

@@ -12,11 +12,14 @@
 //
 // Numerics.  The squares are summed in fp64, so neither large rows overflow nor
 // long ones lose bits, and a bf16 output is the correctly rounded value of the
-// formula for the stored h.  h gamma is exact in fp32 (8 + 8 significant bits);
-// times fp32 1/rms it is within 2 ulp, and a vector with a value that close to
-// a bf16 border is redone with the product's rounding error and the second half
-// of 1/rms.  The MXFP8 codes are those of the bf16 output (mx8_quantize_kernel's
-// rule), so they do not depend on how the sum is split over threads either.
+// formula for the stored h.  For rows of rms 2^-40 to 2^20 h 2^40 stays finite, and
+// p = (h 2^40) gamma is exact in fp32 (8 + 8 significant bits) unless the output is
+// below fp32's normal range too; times fp32 2^-40 / rms it is within 2 ulp, and a
+// vector with a value that close to a bf16 border is redone with the product's
+// rounding error and the second half of 1/rms.  Other rows, and vectors with an
+// infinite result (p may overflow where the output does not), take fp64.  The
+// MXFP8 codes are those of the bf16 output (mx8_quantize_kernel's rule), so they do
+// not depend on how the sum is split over threads either.
 // fp64 costs little here: a bf16 value becomes an fp64 one by moving its bits (a
 // conversion instruction an element cost 1.3 us on 3900 x 1152 rows).
 #include <cuda_fp8.h>
@@ -82,6 +85,19 @@ __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v) {
   return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+// The largest magnitudes of 8 bf16 values, in two halves; NaN drops out.
+__device__ __forceinline__ __nv_bfloat162 max8(const uint4 &v) {
+  return __hmax2(__hmax2(__habs2(as_bf16x2(v.x)), __habs2(as_bf16x2(v.y))),
+                 __hmax2(__habs2(as_bf16x2(v.z)), __habs2(as_bf16x2(v.w))));
+}
+
+// 8 bf16 values times 2^40.
+__device__ __forceinline__ uint4 scaled8(const uint4 &v) {
+  const __nv_bfloat162 s = as_bf16x2(((127u + 40u) << 7) * 0x10001u);
+  return make_uint4(as_u32(__hmul2_rn(as_bf16x2(v.x), s)), as_u32(__hmul2_rn(as_bf16x2(v.y), s)),
+                    as_u32(__hmul2_rn(as_bf16x2(v.z), s)), as_u32(__hmul2_rn(as_bf16x2(v.w), s)));
+}
+
 // An fp32 value that rounds to the same bf16 as v does: v rounded to fp32,
 // moved off a bf16 midpoint to the side v lies on.
 __device__ __forceinline__ float bf16_side(double v) {
@@ -96,7 +112,7 @@ __device__ __forceinline__ float bf16_side(double v) {
 }
 
 // h gamma rstd of 8 bf16 columns, correctly rounded, for rows and values whose
-// fp32 products might leave the normal range.  Out of line: rarely taken, and
+// fp32 products leave the range.  Out of line: rarely taken, and
 // inlined its registers halve the occupancy.
 __device__ __noinline__ uint4 exact8(uint4 h, uint4 gamma, double rstd) {
   float a[8], g[8], o[8];
@@ -239,11 +255,15 @@ __global__ void __launch_bounds__(V == 5 ? 512 : 1024, V == 5 ? 2 : 1)
     if (row_warps > 1 ? __syncthreads_and(fine) : fine) break;
   }
   const double rstd = inverse_root(mean + double(eps));
-  const float rh = float(rstd), rl = float(rstd - double(rh));
+  const float r1 = float(rstd);
+  // rows so large or small that their products might leave the fp32 range (and a
+  // row of zeros without eps, or one with an infinity or NaN) take fp64 throughout
+  const bool wide = sizeof(T) == 2 ? !(r1 > 0x1p-20f && r1 < 0x1p40f)
+                                   : !(r1 > 0x1p-100f && r1 < 0x1p100f);
+  // 1/rms in two halves, without the 2^40 that bf16 products have
+  constexpr float kUnscale = sizeof(T) == 2 ? 0x1p-40f : 1.f;
+  const float rh = r1 * kUnscale, rl = float(rstd - double(r1)) * kUnscale;
   const uint64_t rh2 = f2_pack(rh, rh);
-  // rows so large or small that h gamma might leave the fp32 range (and a row
-  // of zeros without eps, or one with an infinity or NaN) take fp64 throughout
-  const bool wide = !(rh > 0x1p-100f && rh < 0x1p100f);
   if constexpr (MX8) {
     if (row >= ((long long)rows + 127) / 128 * 128) return;  // whole row groups of threads
   } else {
@@ -260,10 +280,11 @@ __global__ void __launch_bounds__(V == 5 ? 512 : 1024, V == 5 ? 2 : 1)
     const bool ok = active && c < nvec;
     const uint4 gv = ok ? __ldg(gr + c) : make_uint4(0, 0, 0, 0);
     float a[N], g[N], o[N];
-    R::unpack(hv[i], a);
     R::unpack(gv, g);
     uint4 packed;
+    __nv_bfloat162 m;
     if constexpr (N == 8) {
+      R::unpack(scaled8(hv[i]), a);
       // o is less than 2 ulp off (1/rms and the product are rounded): only one
       // that is within 1 ulp of a bf16 midpoint may round to another bf16 than
       // the formula's value
@@ -278,18 +299,22 @@ __global__ void __launch_bounds__(V == 5 ? 512 : 1024, V == 5 ? 2 : 1)
         least = __vminu2(least, __byte_perm(__float_as_uint(o[e]), __float_as_uint(o[e + 1]),
                                             0x5410) + 0x80018001u);
       }
-      const bool near = wide || min(least & 0xFFFFu, least >> 16) <= 3u;
       packed = R::pack(o);
+      m = max8(packed);
+      const bool inf = !__hblt2(m, as_bf16x2(0x7F807F80u));
+      const bool near = wide || inf || min(least & 0xFFFFu, least >> 16) <= 3u;
       if (near) {
-        bool small = wide;
+        bool out = wide || inf;
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-          small |= o[e] != 0.f && fabsf(o[e]) < 0x1p-90f;  // the error terms would be subnormal
+          out |= o[e] != 0.f && fabsf(o[e]) < 0x1p-90f;  // the error terms would be subnormal
           o[e] = bf16_side2(a[e], rh, rl);
         }
-        packed = small ? exact8(hv[i], gv, rstd) : R::pack(o);
+        packed = out ? exact8(hv[i], gv, rstd) : R::pack(o);
+        m = max8(packed);
       }
     } else {
+      R::unpack(hv[i], a);
 #pragma unroll
       for (int e = 0; e < N; ++e)
         o[e] = wide ? float(double(a[e]) * double(g[e]) * rstd) : (a[e] * rh) * g[e];
@@ -298,12 +323,9 @@ __global__ void __launch_bounds__(V == 5 ? 512 : 1024, V == 5 ? 2 : 1)
     if constexpr (!MX8) {
       yr[c] = packed;
     } else {
-      if (!ok) packed = make_uint4(0, 0, 0, 0);
+      if (!ok) m = as_bf16x2(0u);  // its codes are not stored
       float q[N];
       R::unpack(packed, q);
-      __nv_bfloat162 m = __hmax2(__habs2(as_bf16x2(packed.x)), __habs2(as_bf16x2(packed.y)));
-      m = __hmax2(m, __habs2(as_bf16x2(packed.z)));
-      m = __hmax2(m, __habs2(as_bf16x2(packed.w)));
       m = __hmax2(m, as_bf16x2(0u));  // NaN drops out, as in the quantiser
       const uint32_t mw = as_u32(m);
       uint32_t amax = max(mw & 0xFFFFu, mw >> 16);  // bf16 magnitudes order as integers
