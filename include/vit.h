@@ -353,7 +353,8 @@ VIT_API vit_status vit_layernorm(vit_ctx *ctx, const void *x, void *y,
  * x, residual, h, y [rows, cols]; gamma [cols].  residual may be NULL (h = x);
  * h may be NULL when the sum is not needed again.  The squares are summed in
  * fp64; a bf16 y is the correctly rounded value of the formula for the stored
- * h.  h and y may each be the same buffer as x or residual (in place), but not
+ * h (a value within 2^-40, relative, of half-way between two bf16 values counts
+ * as half-way: ties to even).  h and y may each be the same buffer as x or residual (in place), but not
  * each other; any other overlap is VIT_ERR_INVALID_ARG.  All pointers 16-byte
  * aligned (fp32 too), eps >= 0.  cols a multiple of 8 (bf16) or 4 (fp32), at
  * most 16384, else VIT_ERR_UNSUPPORTED. */

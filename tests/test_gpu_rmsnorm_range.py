@@ -1,9 +1,10 @@
-"""RMSNorm where h * gamma leaves the fp32 range although the result does not.
+"""RMSNorm where h * gamma leaves the fp32 range although the result does not,
+and where the result lies exactly between two bf16 values.
 
-bf16: y is the formula's value for the stored h rounded once to nearest.  The fp64
-reference is within 2^-50 of the formula, and a random value is closer than that to
-a bf16 midpoint with probability 2^-41, so y is compared bit for bit.  MXFP8 codes
-are those of that y."""
+bf16: y is the formula's value for the stored h rounded once to nearest, ties to
+even.  The fp64 reference is within 2^-50 of the formula, and a random value is
+closer than that to a bf16 midpoint with probability 2^-41, so y is compared bit
+for bit; exact ties are computed by hand.  MXFP8 codes are those of that y."""
 import numpy as np
 import pytest
 import torch
@@ -96,3 +97,30 @@ def test_values_of_every_size(ctx, cols):
     gamma = g.standard_normal(cols) * np.exp2(g.integers(-126, 126, cols).astype(float))
     check(ctx, h, gamma, 0.0)
     check(ctx, h, gamma, 1e-6)
+
+
+def test_exact_ties_go_to_even(ctx):
+    """One value a in 576 columns and no eps: y = 24 gamma sign(a) exactly, which for
+    gamma = m / 64 (m odd, 87 .. 169) lies half-way between two bf16 values."""
+    cols, m = 576, np.arange(87, 170, 2)
+    g = np.random.Generator(np.random.PCG64(5))
+    gamma = np.ones(cols)
+    at = g.permutation(cols)[: len(m)]
+    gamma[at] = m / 64
+    a = NR.to_bf16((1 + g.random(len(m))) * np.exp2(g.integers(-30, 30, len(m)))) * np.where(g.random(len(m)) < 0.5, -1, 1)
+    h, want = np.zeros((len(m), cols)), np.zeros((len(m), cols))
+    h[np.arange(len(m)), at] = a
+    # 3m/8 has 9 significant bits, the last one set: bf16 keeps 8
+    want[np.arange(len(m)), at] = np.sign(a) * np.rint(3 * m / 2) / 4
+    check(ctx, h, gamma, 0.0, want)
+
+
+def test_exact_ties_out_of_range(ctx):
+    """The same in rows whose size sends them through fp64 throughout."""
+    cols, m = 576, np.arange(87, 170, 2)
+    h, gamma, want = np.zeros((len(m), cols)), np.ones(cols), np.zeros((len(m), cols))
+    gamma[: len(m)] = m / 64
+    for r, e in enumerate(np.where(np.arange(len(m)) % 2, 126, -120)):
+        h[r, r] = 1.5 * 2.0 ** e
+        want[r, r] = np.rint(3 * m[r] / 2) / 4
+    check(ctx, h, gamma, 0.0, want)

@@ -12,7 +12,7 @@
 //
 // Numerics.  The squares are summed in fp64, so neither large rows overflow nor
 // long ones lose bits, and a bf16 output is the correctly rounded value of the
-// formula for the stored h.  For rows of rms 2^-40 to 2^20 h 2^40 stays finite, and
+// formula for the stored h (ties to even, within 2^-40).  For rows of rms 2^-40 to 2^20 h 2^40 stays finite, and
 // p = (h 2^40) gamma is exact in fp32 (8 + 8 significant bits) unless the output is
 // below fp32's normal range too; times fp32 2^-40 / rms it is within 2 ulp, and a
 // vector with a value that close to a bf16 border is redone with the product's
@@ -98,6 +98,10 @@ __device__ __forceinline__ uint4 scaled8(const uint4 &v) {
                     as_u32(__hmul2_rn(as_bf16x2(v.z), s)), as_u32(__hmul2_rn(as_bf16x2(v.w), s)));
 }
 
+// Closer to a bf16 midpoint than this, relative, a value counts as half-way: 1/rms
+// is known to about 2^-43, so that exact ties arrive a little off.
+constexpr float kTie = 0x1p-40f;
+
 // An fp32 value that rounds to the same bf16 as v does: v rounded to fp32,
 // moved off a bf16 midpoint to the side v lies on.
 __device__ __forceinline__ float bf16_side(double v) {
@@ -105,8 +109,8 @@ __device__ __forceinline__ float bf16_side(double v) {
   uint32_t u = __float_as_uint(f);
   if ((u & 0xFFFFu) == 0x8000u) {
     const double b = fabs(double(f)), a = fabs(v);
-    u += a > b ? 1u : 0u;
-    u -= a < b ? 1u : 0u;
+    u += a - b > b * kTie ? 1u : 0u;
+    u -= b - a > b * kTie ? 1u : 0u;
   }
   return __uint_as_float(u);
 }
@@ -130,7 +134,8 @@ __device__ __forceinline__ float bf16_side2(float p, float rh, float rl) {
   const float err = fmaf(p, rl, fmaf(p, rh, -hi));
   const float s = hi + err, rest = err - (s - hi);
   uint32_t u = __float_as_uint(s);
-  if ((u & 0xFFFFu) == 0x8000u && rest != 0.f) u += (rest > 0.f) == (s > 0.f) ? 1u : ~0u;
+  if ((u & 0xFFFFu) == 0x8000u && fabsf(rest) > kTie * fabsf(s))
+    u += (rest > 0.f) == (s > 0.f) ? 1u : ~0u;
   return __uint_as_float(u | (__float_as_uint(p) & 0x80000000u));  // -0 + 0 is 0
 }
 
