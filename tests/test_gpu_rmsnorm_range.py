@@ -4,7 +4,9 @@ and where the result lies exactly between two bf16 values.
 bf16: y is the formula's value for the stored h rounded once to nearest, ties to
 even.  The fp64 reference is within 2^-50 of the formula, and a random value is
 closer than that to a bf16 midpoint with probability 2^-41, so y is compared bit
-for bit; exact ties are computed by hand.  MXFP8 codes are those of that y."""
+for bit; exact ties are computed by hand.  MXFP8 codes are those of that y.
+fp32: three roundings from the formula, 2^-24 relative each, and one fp32
+subnormal step for results below the normal range."""
 import numpy as np
 import pytest
 import torch
@@ -124,3 +126,19 @@ def test_exact_ties_out_of_range(ctx):
         h[r, r] = 1.5 * 2.0 ** e
         want[r, r] = np.rint(3 * m[r] / 2) / 4
     check(ctx, h, gamma, 0.0, want)
+
+
+@pytest.mark.parametrize("rows", [5, 700])
+def test_fp32_elements_far_below_their_row(rows):
+    ctx = vit.Context(1152, 16, 72, 4304, vit.F32)
+    g = np.random.Generator(np.random.PCG64(rows))
+    cols = 512
+    h = g.standard_normal((rows, cols))
+    h[:, 1::2] *= np.exp2(-g.integers(60, 149, (rows, cols // 2)).astype(float))
+    h = (h * np.exp2(g.integers(0, 20, (rows, 1)).astype(float))).astype(np.float32)
+    gamma = (g.standard_normal(cols) * np.exp2(g.integers(-20, 100, cols).astype(float))).astype(np.float32)
+    y = torch.empty(rows, cols, device="cuda")
+    ctx.rmsnorm(to_dev(h, "f32"), to_dev(gamma, "f32"), y, eps=0.0)
+    ref = NR.rmsnorm(h.astype(np.float64), gamma.astype(np.float64), 0.0)
+    assert np.all(np.abs(from_dev(y) - ref) <= 3.01 * 2.0 ** -24 * np.abs(ref) + 2.0 ** -148)
+    ctx.close()

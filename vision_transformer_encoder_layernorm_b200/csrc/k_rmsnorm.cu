@@ -321,8 +321,11 @@ __global__ void __launch_bounds__(V == 5 ? 512 : 1024, V == 5 ? 2 : 1)
     } else {
       R::unpack(hv[i], a);
 #pragma unroll
-      for (int e = 0; e < N; ++e)
-        o[e] = wide ? float(double(a[e]) * double(g[e]) * rstd) : (a[e] * rh) * g[e];
+      for (int e = 0; e < N; ++e) {
+        const float u = a[e] * rh;  // at most sqrt(cols)
+        const bool far = fabsf(u) < 0x1p-126f && a[e] != 0.f;  // it has lost bits, and g may be large
+        o[e] = wide || far ? float(double(a[e]) * double(g[e]) * rstd) : u * g[e];
+      }
       packed = R::pack(o);
     }
     if constexpr (!MX8) {
