@@ -24,5 +24,12 @@ __device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity) {
   }
 }
 
+// After an abort: time for copies into shared memory that no barrier is waited on for.
+__device__ __forceinline__ void settle() {
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < 2000000ull) {  // 2 ms
+  }
+}
+
 }  // namespace gemm
 }  // namespace vit

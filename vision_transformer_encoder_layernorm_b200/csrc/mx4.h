@@ -28,9 +28,12 @@ cudaError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, i
                                   void *y, cudaStream_t st);
 
 // y[M, N] (bf16) = epi(deq(A) . deq(W)^T + b): A codes/scales [M, K], W
-// codes/scales [N, K]; epi: kEpiBias, kEpiGelu or kEpiResidual.
+// codes/scales [N, K]; epi: kEpiBias, kEpiGelu or kEpiResidual.  lost_tx: fault
+// injection for the watchdog tests (0 in normal use), the bytes that a stage barrier
+// expects beyond those that arrive.
 cudaError_t launch_gemm_mx4(const uint8_t *a_codes, const uint8_t *a_scales, const uint8_t *w_codes,
                             const uint8_t *w_scales, const void *b, const void *res, void *y, int M,
-                            int N, int K, int epi, int num_sms, int *status, cudaStream_t st);
+                            int N, int K, int epi, int num_sms, int *status, cudaStream_t st,
+                            uint32_t lost_tx = 0);
 
 }  // namespace vit

@@ -72,8 +72,8 @@ struct vit_ctx {
   cudaStream_t cap_stream = nullptr;
   bool cap_prof_on = false;
   long long cap_launches0 = 0;
-  // fault injection (vit_debug_lost_tx): extra bytes the one-CTA GEMM's
-  // stage barriers wait for; 0 in normal use
+  // fault injection (vit_debug_lost_tx): extra bytes that stage barriers of the
+  // one-CTA GEMM and the MXFP4 GEMM wait for; 0 in normal use
   uint32_t debug_lost_tx = 0;
 };
 
@@ -1206,7 +1206,7 @@ vit_status vit_linear_mx4(vit_ctx *ctx, const void *a_codes, const void *a_scale
                            static_cast<const uint8_t *>(w_codes),
                            static_cast<const uint8_t *>(w_scales), bias,
                            epi == VIT_EPI_BIAS_RESIDUAL ? residual : nullptr, y, M, N, K, int(epi),
-                           ctx->num_sms, ctx->d_status, st);
+                           ctx->num_sms, ctx->d_status, st, ctx->debug_lost_tx);
   }));
 }
 
