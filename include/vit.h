@@ -578,7 +578,7 @@ VIT_API vit_status vit_get_last_device_status(vit_ctx *ctx);
 /* Fault injection for tests of the bounded waits; the pages have no
  * counterpart.  With bytes > 0, every later one-CTA GEMM launch of this
  * context (vit_linear with at most 128 rows always takes that kernel) and every
- * split tile of vit_linear_mx4 (in the last CTA of its cluster)
+ * launch of vit_linear_mx4 (a split tile: in the last CTA of its cluster)
  * announces `bytes` more per pipeline stage than its copies deliver, so the
  * stage barrier never completes.  The kernel's waits are bounded (2 s): it
  * winds down, waits for its copies, frees its tensor memory and records

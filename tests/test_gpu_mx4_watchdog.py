@@ -62,3 +62,22 @@ def test_split_tile_that_lost_bytes_is_not_written(monkeypatch, tile, M, N, K, e
     status, _, y = c.run()
     assert status == 0 and torch.equal(y, want)
     c.ctx.close()
+
+
+@pytest.mark.parametrize("tile", ["1x128", "2x128", "2x192", "2x256"])
+@pytest.mark.parametrize("M,N,K,epi", [
+    (300, 264, 130, vit.EPI_BIAS),                # every copy is issued before a wait runs out
+    (300, 392, 4304, vit.EPI_BIAS_RESIDUAL)])     # the producer waits too, residual copies in flight
+def test_tiles_that_lost_bytes_time_out(monkeypatch, tile, M, N, K, epi):
+    monkeypatch.setenv("VIT_MX4_TILE", tile)
+    c = Call(M, N, K, epi)
+    status, _, want = c.run()
+    assert status == 0
+    c.ctx.debug_lost_tx(16)
+    status, waited, _ = c.run()
+    assert status == TIMEOUT and 1.5 <= waited <= 30.0, (status, waited)
+    c.ctx.debug_lost_tx(0)
+    for _ in range(3):
+        status, _, y = c.run()
+        assert status == 0 and torch.equal(y, want)
+    c.ctx.close()

@@ -171,7 +171,7 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::kThreads), 1)
                     const __grid_constant__ CUtensorMap tmSb,
                     const __grid_constant__ CUtensorMap tmR, const __grid_constant__ CUtensorMap tmY,
                     const __nv_bfloat16 *__restrict__ bias, int M, int N, int K, int *status,
-                    const __grid_constant__ Prefetch pre) {
+                    const __grid_constant__ Prefetch pre, uint32_t lost_tx) {
   using CF = Cfg<BN, PAIR>;
   constexpr int kCtas = PAIR ? 2 : 1, kRows = kCtas * BM;
   extern __shared__ uint8_t smem_raw[];
@@ -251,7 +251,10 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::kThreads), 1)
           uint8_t *sa = smem + size_t(stage) * CF::kStageBytes;
           const int n0 = nb * BN + rank * CF::kBRows;
           uint32_t full = smem_u32(&bars->full[stage]);
-          if (rank == 0) mbar_arrive_expect_tx(&bars->full[stage], kCtas * CF::kStageBytes);
+          // lost_tx > 0 only under fault injection (vit_debug_lost_tx): the stage then
+          // waits for bytes that no copy delivers
+          if (rank == 0)
+            mbar_arrive_expect_tx(&bars->full[stage], kCtas * CF::kStageBytes + lost_tx);
           if constexpr (PAIR) {
             full = map_to_cta(&bars->full[stage], 0);
             tma_load_2d_pair(sa, &tmA, full, kb * (kBK / 2), mb * BM);
@@ -268,17 +271,9 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::kThreads), 1)
           if (++stage == CF::kStages) { stage = 0; phase ^= 1; }
         }
       }
-      if (!ok) {
-        if (rank == 0) {
-          for (int s = 0; s < CF::kStages; ++s)
-            if (issued_mask & (1u << s)) gemm::drain_wait(&bars->full[s], (issued_parity >> s) & 1);
-        } else {
-          // this CTA's copies complete on the leader's barriers: give them time
-          const uint64_t t0 = globaltimer_ns();
-          while (globaltimer_ns() - t0 < 2000000ull) {
-          }
-        }
-      }
+      if (!ok && rank == 0)
+        for (int s = 0; s < CF::kStages; ++s)
+          if (issued_mask & (1u << s)) gemm::drain_wait(&bars->full[s], (issued_parity >> s) & 1);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader)
@@ -411,7 +406,13 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::kThreads), 1)
     if constexpr (PAIR) tmem_dealloc_pair(tmem, CF::kTmemCols);
     else tmem_dealloc(tmem, CF::kTmemCols);
   }
-  if (threadIdx.x == 0 && bars->abort_flag) report_status(status, kDevTimeout);
+  if (threadIdx.x == 0 && bars->abort_flag) {
+    // The CTA stays for copies that nobody has waited for: those that a producer had
+    // issued before another role gave up, and rank 1's, which complete on the
+    // leader's barriers.  (If the leader gives up, rank 1 does: it misses a tile.)
+    gemm::settle();
+    report_status(status, kDevTimeout);
+  }
 }
 
 // Few tiles and a long K: a cluster of SPLIT CTAs shares one 128 x 128 tile, each
@@ -420,7 +421,8 @@ __global__ void __launch_bounds__((Cfg<BN, PAIR>::kThreads), 1)
 // finishes columns [r, r + 1) 128 / SPLIT, adding the partials of all CTAs in
 // rank order over the cluster's shared memory, so the result does not depend on
 // which CTA is done first.  A CTA that gave up (a lost arrival) leaves kGaveUp in
-// place of its sums, and what they belong to is not written.  No CTA is persistent: the grid is one cluster a tile.
+// place of its sums, and what they belong to is not written.  No CTA is persistent:
+// the grid is one cluster a tile.
 constexpr uint32_t kGaveUp = 0xFFC0DEADu;  // a NaN that no MMA produces (theirs is 7FFFFFFF)
 template <int EPI, int SPLIT>
 __global__ void __launch_bounds__((Cfg<128, false>::kThreads), 1)
@@ -590,7 +592,10 @@ __global__ void __launch_bounds__((Cfg<128, false>::kThreads), 1)
     tc_fence_after();
     tmem_dealloc(tmem, CF::kTmemCols);
   }
-  if (threadIdx.x == 0 && bars->abort_flag) report_status(status, kDevTimeout);
+  if (threadIdx.x == 0 && bars->abort_flag) {
+    gemm::settle();  // as above
+    report_status(status, kDevTimeout);
+  }
 }
 
 struct Args {
@@ -684,7 +689,7 @@ cudaError_t run(const Args &g) {
   if (tiles > 0x7FFFFFFFll - 4ll * g.num_sms) return cudaErrorInvalidValue;
   const int workers = int(std::min<long long>(tiles, most));
   return launch_pdl(kern, dim3(workers * kCtas), dim3(CF::kThreads), CF::kSmemBytes, g.st, kCtas, m.a,
-                    m.b, m.sa, m.sb, m.res, m.y, g.bias, g.M, g.N, g.K, g.status, pre);
+                    m.b, m.sa, m.sb, m.res, m.y, g.bias, g.M, g.N, g.K, g.status, pre, g.lost_tx);
 }
 
 template <int EPI, int SPLIT>
