@@ -19,7 +19,7 @@ namespace vit {
 
 inline size_t mx8_row_bytes(int K) { return (size_t(K) + 15) / 16 * 16; }
 inline size_t mx8_scale_bytes(int rows, int K) {
-  return size_t((rows + 127) / 128) * size_t((K + 127) / 128) * 512;
+  return (size_t(rows) + 127) / 128 * ((size_t(K) + 127) / 128) * 512;
 }
 
 // bf16 [rows, K] (row stride K) -> codes and scales.
