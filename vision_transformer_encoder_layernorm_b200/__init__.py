@@ -8,13 +8,17 @@ This module only marshals arguments: every step runs in the CUDA kernels of
 ``libvit.so``.  There is no fallback; importing fails loudly when the library
 has not been built (``python vision_transformer_encoder_layernorm_b200/build.py``).
 Most calls go through ctypes; RMSNorm, MXFP4 and three-axis RoPE, which also check
-their tensors, through the extension module ``_marshal`` (csrc/marshal.c).
+their tensors, through the extension module ``_marshal`` (csrc/marshal.c), loaded
+by the first of them.
 Tensors are PyTorch tensors (device memory and streams only).
 """
 from __future__ import annotations
 
 import ctypes
+import functools
+import importlib.util
 import os
+import sysconfig
 from typing import Optional, Sequence
 
 __all__ = [
@@ -155,13 +159,19 @@ def _load():
     return h
 
 
+@functools.lru_cache(maxsize=None)
 def _load_marshal():
-    path = os.path.join(os.path.dirname(LIB_PATH), "_marshal.so")
+    # by its full name: a module of that name without a suffix, or with another's, is
+    # for another Python
+    path = os.path.join(os.path.dirname(LIB_PATH),
+                        "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
     if not os.path.exists(path):
         raise ImportError(
             f"{path} is missing: build it with "
             "`python vision_transformer_encoder_layernorm_b200/build.py`")
-    from . import _marshal as m
+    spec = importlib.util.spec_from_file_location(__name__ + "._marshal", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
     m.bind(*(ctypes.cast(getattr(lib, name), _P).value for name in (
         "vit_rmsnorm", "vit_rmsnorm_mx8", "vit_mx4_quantize", "vit_mx4_dequantize",
         "vit_linear_mx4", "vit_rope3d")))
@@ -169,7 +179,6 @@ def _load_marshal():
 
 
 lib = _load()
-_marshal = _load_marshal()
 
 
 def _ptr(t) -> Optional[int]:
@@ -282,7 +291,7 @@ class Context:
         if name != "_calls":
             raise AttributeError(name)
         import torch
-        self._calls = _marshal.Calls(
+        self._calls = _load_marshal().Calls(
             self._h.value if isinstance(self._h, _P) else self._h,
             torch.bfloat16 if self.cfg.dtype == BF16 else torch.float32, torch.uint8, torch.int32,
             torch._C._cuda_getCurrentRawStream, self._device, self.cfg.ln_eps, self.cfg.head_dim)

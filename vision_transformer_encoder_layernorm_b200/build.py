@@ -1,4 +1,5 @@
-"""Builds libvit.so in-tree for sm_100a with nvcc (no GPU needed).
+"""Builds libvit.so in-tree for sm_100a with nvcc (no GPU needed), and the
+binding's extension module _marshal with a C compiler, for the running Python.
 
     python vision_transformer_encoder_layernorm_b200/build.py [--force]
 
@@ -17,7 +18,8 @@ import sysconfig
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libvit.so")
-MARSHAL = os.path.join(HERE, "_marshal.so")  # CPython extension: argument marshalling
+# CPython extension: argument marshalling; its name says which Python it is for
+MARSHAL = os.path.join(HERE, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["vit_api.cu", "k_rows.cu", "k_simt.cu", "k_gemm_tc.cu", "k_attn_tc.cu", "k_embed.cu", "k_mx8.cu",
@@ -37,10 +39,10 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(MARSHAL):
+def _stale(target: str) -> bool:
+    if not os.path.exists(target):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
+    t = os.path.getmtime(target)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     deps += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     deps.append(os.path.abspath(__file__))
@@ -48,7 +50,7 @@ def _stale() -> bool:
 
 
 def build_marshal(verbose: bool = False) -> str:
-    """The binding's extension module, for the running Python."""
+    """The binding's extension module, for the running Python (needs its headers)."""
     out_tmp = MARSHAL + ".tmp"
     cmd = [os.environ.get("CC") or "gcc", "-O2", "-shared", "-fPIC", "-Wall",
            "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "marshal.c"),
@@ -61,9 +63,17 @@ def build_marshal(verbose: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    """Compiles every CUDA source into libvit.so (skipped when up to date)."""
-    if not force and not _stale():
-        return LIB
+    """The library, then the extension module (each skipped when up to date).  If the
+    module fails the library is there all the same: most calls need no more."""
+    if force or _stale(LIB):
+        build_lib(verbose, extra)
+    if force or _stale(MARSHAL):
+        build_marshal(verbose)
+    return LIB
+
+
+def build_lib(verbose: bool = False, extra=()) -> str:
+    """Compiles every CUDA source into libvit.so."""
     tmp_dir = os.path.join(HERE, "_build")
     os.makedirs(tmp_dir, exist_ok=True)
     objs, cmds = [], []
@@ -77,7 +87,6 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         if verbose:
             print(" ".join(cmd), flush=True)
         procs.append(subprocess.Popen(cmd))
-    build_marshal(verbose)
     failed = [c for c, p in zip(cmds, procs) if p.wait() != 0]
     if failed:
         raise RuntimeError("nvcc failed: " + " ".join(failed[0]))
