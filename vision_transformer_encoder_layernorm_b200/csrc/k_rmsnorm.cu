@@ -389,9 +389,11 @@ cudaError_t pick(const void *x, const void *res, const void *gamma, void *h, voi
   // MX8 threads also cover the padding columns of the last 128-column block
   const int nvec = MX8 ? (cols + 127) / 128 * 16 : cols / RowVec<T>::N;
 #define VIT_RMS(V) return run<T, MX8, V>(x, res, gamma, h, y, rows, cols, eps, codes, scales, nvec, st)
-  const bool many = sizeof(T) == 2 && (long long)rows * nvec > 1024ll * num_sms;
-  if (many && nvec > 64 && nvec <= 2560) VIT_RMS(5);
-  if (many && nvec <= 64) VIT_RMS(2);
+  if constexpr (sizeof(T) == 2) {
+    const bool many = (long long)rows * nvec > 1024ll * num_sms;
+    if (many && nvec > 64) VIT_RMS(5);
+    if (many) VIT_RMS(2);
+  }
   if (nvec <= 1024) VIT_RMS(1);
   if (nvec <= 2048) VIT_RMS(2);
   if constexpr (RowVec<T>::N == 4)
