@@ -354,15 +354,19 @@ VIT_API vit_status vit_layernorm(vit_ctx *ctx, const void *x, void *y,
  * h may be NULL when the sum is not needed again.  The squares are summed in
  * fp64; a bf16 y is the correctly rounded value of the formula for the stored
  * h (a value within 2^-40, relative, of half-way between two bf16 values counts
- * as half-way: ties to even).  h and y may each be the same buffer as x or residual (in place), but not
- * each other; any other overlap is VIT_ERR_INVALID_ARG.  All pointers 16-byte
- * aligned (fp32 too), eps >= 0.  cols a multiple of 8 (bf16) or 4 (fp32), at
- * most 16384, else VIT_ERR_UNSUPPORTED. */
+ * as half-way: ties to even), an fp32 y within three roundings of it.  h and y may
+ * each be the same buffer as x or residual (in place), but not each other; any
+ * other overlap is VIT_ERR_INVALID_ARG.  All pointers 16-byte aligned (fp32 too),
+ * eps >= 0.  cols a multiple of 8 (bf16) or 4 (fp32), at most 16384, else
+ * VIT_ERR_UNSUPPORTED. */
 VIT_API vit_status vit_rmsnorm(vit_ctx *ctx, const void *x, const void *residual,
                                const void *gamma, void *h, void *y, int rows, int cols, float eps,
                                void *stream);
 
-/* Epilogues of vit_linear */
+/* Epilogues of vit_linear.  GELU in a bf16 context (the MXFP8 and MXFP4 layers
+ * too) takes the hardware tanh, which is within 2^-10.9 of the value, relative:
+ * GELU(u) is off by up to |u| 2^-11.9 before its rounding, which is 1% of the value
+ * at u = -2 and 20% at u = -3, where 1 + tanh cancels. */
 typedef enum {
   VIT_EPI_BIAS = 0,           /* y = x W^T + b                               */
   VIT_EPI_BIAS_GELU = 1,      /* y = GELU_tanh(x W^T + b)                    */
@@ -475,10 +479,14 @@ VIT_API vit_status vit_linear_mx8(vit_ctx *ctx, const void *a_codes, const void 
  * codes  : [rows, vit_mx4_row_bytes(K)] bytes, two elements a byte: element
  *          (r, k) in the low (even k) or high (odd k) nibble of byte
  *          r * row_bytes + k / 2.  vit_mx4_row_bytes(K) = 16 ceil(K / 32);
- *          the nibbles past K hold zero.
+ *          the nibbles past K hold zero (vit_linear_mx4 reads the one that an
+ *          odd K leaves in its last byte, and none behind that byte).
  * scales : vit_mx4_scale_bytes(rows, K) bytes, the layout of the MXFP8
  *          scales (512-byte blocks of 128 rows x 128 columns).  Byte 255 (NaN)
- *          marks a group that holds a NaN.
+ *          marks a group that holds a NaN.  Bytes of rows or groups past the
+ *          matrix hold 127: vit_linear_mx4 multiplies the zeros past K by those of
+ *          groups up to the next multiple of 64 columns, and a 255 there would
+ *          make its row's results NaN.
  * All buffers belong to the caller; device pointers 16-byte aligned. */
 VIT_API size_t vit_mx4_row_bytes(int K);
 VIT_API size_t vit_mx4_scale_bytes(int rows, int K);

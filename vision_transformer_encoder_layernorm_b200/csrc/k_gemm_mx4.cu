@@ -730,18 +730,23 @@ cudaError_t run_epi(const Args &g, int epi) {
   }
 }
 
-// The tile's shape by a cost model, in microseconds as measured over 3900 x
-// {1152, 3456, 4304} x {1152, 4304}, 960 x 4304 x 1152, 10936 x 1152 x 4304 and
-// 8192 x 4096 x 8192: a round over the SMs takes a tile's k-blocks or its
+// The tile's shape by a cost model.  Its constants (microseconds) are fitted to the
+// order of the shapes over 3900 x {1152, 3456, 4304} x {1152, 4304}, 960 x 4304 x
+// 1152, 10936 x 1152 x 4304 and 8192 x 4096 x 8192; its sums are not times (3900 x
+// 4304 x 1152: 11.2 for 15.4 us; 10936 x 1152 x 4304: 26.6 for 35.9; 8192 x 4096 x
+// 8192: 106 for 100), since the launch and rows that straddle lines are not in them.
+// A round over the SMs takes a tile's k-blocks or its
 // epilogue, whichever is longer (accumulators that share columns add a wait); the
 // first round's k-blocks and the last one's epilogue are not overlapped, a pair
 // starts later, and joining a split tile takes time by its rows and parts.
-//  - One CTA wins with few k-blocks and tiles (960 x 4304 x 1152: 6.8 us, pairs
-//    7.6 to 8.5; 3900 x 1152 x 1152: 9.0 against 9.3);
+//  - One CTA wins with few k-blocks and tiles (960 x 4304 x 1152: 6.9 us, pairs
+//    7.7 to 8.2; 3900 x 1152 x 1152: 9.1 against 9.4);
 //  - 192 columns for the wide projections (3900 x 4304 x 1152: 15.4, 128 columns
-//    17.5, 256 16.0, one CTA 18.3);
-//  - 256 for the most work per byte (10936 x 1152 x 4304: 35.4 against 42.0 at 128;
-//    8192 x 4096 x 8192: 99 against 122);
+//    17.9, 256 15.8, one CTA 18.1);
+//  - 256 for the most work per byte (10936 x 1152 x 4304: 35.9, 192 columns 36.7, 128
+//    41.7; 8192 x 4096 x 8192: 100, 109, 123);
+//  - where it errs: 960 x 1152 x 4304 takes 10.6 us split over 2 CTAs, pairs of 128
+//    columns 9.3; 10936 x 4304 x 1152 35.4 with 192 columns, 256 34.4;
 //  - split tiles for few rows over a long K (1 x 1152 x 4304: 7.8, over 8 CTAs 4.1;
 //    64 rows: 9.0, over 4 CTAs 7.3, over 8 8.6; 1 x 3456 x 1152: 3.7 either way).
 struct Shape {

@@ -6,8 +6,8 @@
 // Bound: HBM.  x and residual are read once, h and y written once (8 bytes a
 // bf16 element, 7 with MXFP8 codes); the row stays in registers between the
 // sum of squares and the output.  10936 x 1152 with residual takes 19.9 us (5070
-// GB/s, 79% of the measured copy rate), 3900 x 1152 to MXFP8 10.4 us: there all rows
-// are resident at once, and a warp's 1200 instructions after its loads are what is
+// GB/s, 79% of the measured copy rate), 3900 x 1152 to MXFP8 10.7 us: there all rows
+// are resident at once, and a warp's 1250 instructions after its loads are what is
 // left.
 //
 // Numerics.  The squares are summed in fp64, so neither large rows overflow nor
